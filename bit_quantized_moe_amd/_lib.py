@@ -8,6 +8,7 @@ bit_quantized_moe_amd.build); without it every call raises.
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -17,6 +18,7 @@ LIB_PATH = os.path.join(HERE, "libbqm.so")
 
 FMT_NVFP4 = 1
 FMT_NF4 = 2
+FMT_MXFP4 = 3
 SCALE_PER_TENSOR = 0
 SCALE_PER_ROW = 1
 
@@ -31,7 +33,9 @@ STATUS = {0: "BQM_OK", -1: "BQM_ERR_INVALID_ARG", -2: "BQM_ERR_SHAPE", -3: "BQM_
 EXPORTS = ["bqm_abi_version", "bqm_last_error", "bqm_quantize_nvfp4_workspace_size",
            "bqm_quantize_nvfp4", "bqm_quantize_nvfp4_noalloc", "bqm_quantize_nf4", "bqm_dequantize", "bqm_route",
            "bqm_permute_workspace_size", "bqm_permute", "bqm_moe_workspace_size", "bqm_moe_fwd",
-           "bqm_moe_dgrad", "bqm_moe_dgrad_colwise", "bqm_lora_grad", "bqm_nf4_nest"]
+           "bqm_moe_dgrad", "bqm_moe_dgrad_colwise", "bqm_lora_grad", "bqm_nf4_nest", "bqm_quantize_mxfp4",
+           "bqm_mxfp4_gemm", "bqm_mxfp4_dgrad", "bqm_swiglu_ckpt_fwd", "bqm_swiglu_ckpt_bwd",
+           "bqm_router_loss_workspace_size", "bqm_router_loss", "bqm_router_grad"]
 
 
 class BQMError(RuntimeError):
@@ -88,6 +92,14 @@ def load(path: str = LIB_PATH):
         "bqm_moe_dgrad_colwise": (C.c_int, [C.POINTER(MoEDescC), C.POINTER(QTensorC), C.POINTER(QTensorC), vp, vp,
                                             sz, vp, vp, vp]),
         "bqm_lora_grad": (C.c_int, [C.POINTER(MoEDescC), vp, vp, vp, sz, vp, vp, vp, vp, vp]),
+        "bqm_quantize_mxfp4": (C.c_int, [vp, C.POINTER(QTensorC), vp]),
+        "bqm_mxfp4_gemm": (C.c_int, [C.POINTER(QTensorC), C.POINTER(QTensorC), vp, vp, i32, i64, vp, vp]),
+        "bqm_mxfp4_dgrad": (C.c_int, [C.POINTER(QTensorC), vp, i64, vp, vp, i32, i64, vp, vp]),
+        "bqm_swiglu_ckpt_fwd": (C.c_int, [vp, i64, i64, vp, vp, vp, vp, C.POINTER(QTensorC), vp]),
+        "bqm_swiglu_ckpt_bwd": (C.c_int, [vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, vp]),
+        "bqm_router_loss_workspace_size": (sz, [i64, i32]),
+        "bqm_router_loss": (C.c_int, [vp, vp, vp, i64, i32, i32, vp, vp, vp, sz, vp]),
+        "bqm_router_grad": (C.c_int, [vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -146,6 +158,9 @@ def alloc_qtensor(fmt, n_mat, rows, cols, device="cuda", scale_mode=SCALE_PER_TE
         scales = torch.empty((n_mat, rows, cols // 16), dtype=torch.uint8, device=device)
         n = n_mat if scale_mode == SCALE_PER_TENSOR else n_mat * rows
         s_dec = torch.empty((max(n, 1),), dtype=torch.float32, device=device)
+    elif fmt == FMT_MXFP4:
+        scales = torch.empty((n_mat, rows, cols // 32), dtype=torch.uint8, device=device)
+        s_dec = None
     elif nested:
         scales = torch.empty((n_mat, rows, cols // 64), dtype=torch.uint8, device=device)
         s_dec = torch.empty((max(n_mat, 1), 1 + nf4_nest_groups(rows, cols)), dtype=torch.float32, device=device)
@@ -157,8 +172,8 @@ def alloc_qtensor(fmt, n_mat, rows, cols, device="cuda", scale_mode=SCALE_PER_TE
 
 def quantize_stack(w, fmt: str, stream=None) -> QTensor:
     """Allocate and fill a rowwise-quantized stack from a bf16 [n_mat, rows, cols] tensor:
-    fmt "nvfp4" (per-tensor scale, Four-Over-Six), "nf4" or "nf4_nested" (NF4, then
-    bqm_nf4_nest; the nested stack keeps the plain codes).  Allocation plus the library
+    fmt "nvfp4" (per-tensor scale, Four-Over-Six), "mxfp4", "nf4" or "nf4_nested" (NF4,
+    then bqm_nf4_nest; the nested stack keeps the plain codes).  Allocation plus the library
     calls, nothing else."""
     import torch
     n_mat, rows, cols = w.shape
@@ -168,6 +183,8 @@ def quantize_stack(w, fmt: str, stream=None) -> QTensor:
         ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=w.device)
         bqm_quantize_nvfp4(w, 1, None, q, ws, stream)
         return q
+    if fmt == "mxfp4":
+        return bqm_quantize_mxfp4(w, alloc_qtensor(FMT_MXFP4, n_mat, rows, cols, device=w.device), stream)
     if fmt not in ("nf4", "nf4_nested"):
         raise ValueError(f"unknown weight format {fmt!r}")
     q = alloc_qtensor(FMT_NF4, n_mat, rows, cols, device=w.device)
@@ -304,3 +321,132 @@ def bqm_lora_grad(d: MoEDesc, x, dy, ws, dA_gu, dB_gu, dA_dn, dB_dn, stream=None
     dc = d.c()
     _check(load().bqm_lora_grad(C.byref(dc), _ptr(x), _ptr(dy), _ptr(ws), ws.numel() * ws.element_size(),
                                 _ptr(dA_gu), _ptr(dB_gu), _ptr(dA_dn), _ptr(dB_dn), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------
+# experts over MXFP4 and the router's training.  These calls take their sizes from the
+# tensors, so the tensors' types, shapes and layout are checked here; everything else is
+# checked behind the C ABI.
+# ----------------------------------------------------------------------------
+def _dense(name, t, dtype, shape=None):
+    """t (None passes) if it is a contiguous tensor of that dtype and number of elements."""
+    if t is None:
+        return None
+    import torch
+    if t.dtype is not getattr(torch, dtype):
+        raise BQMError(-1, f"{name}: dtype {t.dtype}, torch.{dtype} needed")
+    if not t.is_contiguous():
+        raise BQMError(-2, f"{name}: not contiguous")
+    if shape is not None and t.numel() != math.prod(shape):
+        raise BQMError(-2, f"{name}: shape {tuple(t.shape)}, {tuple(shape)} needed")
+    return t
+
+
+def _dense_q(name, q: QTensor, blk=32):
+    _dense(name + ".codes", q.codes, "uint8", (q.n_mat, q.rows, q.cols // 2))
+    _dense(name + ".scales", q.scales, "uint8", (q.n_mat, q.rows, q.cols // blk))
+    return q.c()
+
+
+def bqm_quantize_mxfp4(x, out: QTensor, stream=None):
+    """bf16 x [n_mat, rows, cols] -> out, an MXFP4 stack (returned)."""
+    lib = load()
+    _dense("x", x, "bfloat16", (out.n_mat, out.rows, out.cols))
+    qc = _dense_q("out", out)
+    _check(lib.bqm_quantize_mxfp4(_ptr(x), C.byref(qc), _stream(stream)))
+    return out
+
+
+def bqm_mxfp4_gemm(x: QTensor, w: QTensor, offsets, perm, k, y, stream=None):
+    """y [R, N] = rows of x [1, rows, K] times their experts' w [E, N, K]; perm None: rows
+    are in routed order already.  R is y's first dimension."""
+    lib = load()
+    R = y.shape[0]
+    xc, wc = _dense_q("x", x), _dense_q("w", w)
+    _dense("offsets", offsets, "int32", (w.n_mat + 1,))
+    _dense("perm", perm, "int32", (R,))
+    _dense("y", y, "bfloat16", (R, w.rows))
+    _check(lib.bqm_mxfp4_gemm(C.byref(xc), C.byref(wc), _ptr(offsets), _ptr(perm), k, R, _ptr(y), _stream(stream)))
+    return y
+
+
+def bqm_mxfp4_dgrad(w: QTensor, dy, offsets, perm, k, dx, stream=None):
+    """dx [R, K] = rows of dy [rows, N] times their experts' DQ(w) [E, N, K]."""
+    lib = load()
+    R = dx.shape[0]
+    wc = _dense_q("w", w)
+    _dense("dy", dy, "bfloat16", (dy.shape[0], w.rows))
+    _dense("offsets", offsets, "int32", (w.n_mat + 1,))
+    _dense("perm", perm, "int32", (R,))
+    _dense("dx", dx, "bfloat16", (R, w.cols))
+    _check(lib.bqm_mxfp4_dgrad(C.byref(wc), _ptr(dy), dy.shape[0], _ptr(offsets), _ptr(perm), k, R, _ptr(dx),
+                               _stream(stream)))
+    return dx
+
+
+def bqm_swiglu_ckpt_fwd(h, h8, h8_scales, a=None, aq: Optional[QTensor] = None, n_rows=None, stream=None):
+    """h [R, 2I] -> the 8-bit copy h8 [R, 2I], h8_scales [R, 2I/32]; a [R, I], aq [1, R, I]
+    where given.  n_rows: a one-element int32 tensor (offsets[E:], say)."""
+    lib = load()
+    R, I = h.shape[0], h.shape[1] // 2
+    _dense("h", h, "bfloat16", (R, 2 * I))
+    _dense("h8", h8, "uint8", (R, 2 * I))
+    _dense("h8_scales", h8_scales, "uint8", (R, 2 * I // 32))
+    _dense("a", a, "bfloat16", (R, I))
+    _dense("n_rows", n_rows, "int32", (1,))
+    qc = None if aq is None else C.byref(_dense_q("aq", aq))
+    _check(lib.bqm_swiglu_ckpt_fwd(_ptr(h), R, I, _ptr(n_rows), _ptr(h8), _ptr(h8_scales), _ptr(a), qc,
+                                   _stream(stream)))
+
+
+def bqm_swiglu_ckpt_bwd(h8, h8_scales, da, perm, topk_w, dh, dtopk_w=None, n_rows=None, stream=None):
+    """The 8-bit copy and da [R, I] -> dh [R, 2I], dtopk_w [R] (or [T, k]) where given."""
+    lib = load()
+    R, I = da.shape
+    _dense("h8", h8, "uint8", (R, 2 * I))
+    _dense("h8_scales", h8_scales, "uint8", (R, 2 * I // 32))
+    _dense("da", da, "bfloat16", (R, I))
+    _dense("perm", perm, "int32", (R,))
+    _dense("topk_w", topk_w, "float32", (R,))
+    _dense("dh", dh, "bfloat16", (R, 2 * I))
+    _dense("dtopk_w", dtopk_w, "float32", (R,))
+    _dense("n_rows", n_rows, "int32", (1,))
+    _check(lib.bqm_swiglu_ckpt_bwd(_ptr(h8), _ptr(h8_scales), _ptr(da), _ptr(perm), _ptr(topk_w), R, I, _ptr(n_rows),
+                                   _ptr(dh), _ptr(dtopk_w), _stream(stream)))
+    return dh
+
+
+def bqm_router_loss_workspace_size(T, E) -> int:
+    return load().bqm_router_loss_workspace_size(T, E)
+
+
+def bqm_router_loss(logits, topk_idx, valid, counts, loss, ws, stream=None):
+    """logits [T, E], topk_idx [T, k] (valid uint8 [T] or None) -> counts int32 [E+1], loss
+    float32 [2] = (balance loss, z-loss)."""
+    lib = load()
+    (T, E), k = logits.shape, topk_idx.shape[1]
+    _dense("logits", logits, "float32")
+    _dense("topk_idx", topk_idx, "int32", (T, k))
+    _dense("valid", valid, "uint8", (T,))
+    _dense("counts", counts, "int32", (E + 1,))
+    _dense("loss", loss, "float32", (2,))
+    wsb = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib.bqm_router_loss(_ptr(logits), _ptr(topk_idx), _ptr(valid), T, E, k, _ptr(counts), _ptr(loss), _ptr(ws),
+                               wsb, _stream(stream)))
+
+
+def bqm_router_grad(logits, topk_idx, valid, counts, dtopk_w, dloss, renorm, dlogits, stream=None):
+    """dlogits [T, E] of the losses (times dloss [2], or None) and of topk_w (times dtopk_w
+    [T, k], or None)."""
+    lib = load()
+    (T, E), k = logits.shape, topk_idx.shape[1]
+    _dense("logits", logits, "float32")
+    _dense("topk_idx", topk_idx, "int32", (T, k))
+    _dense("valid", valid, "uint8", (T,))
+    _dense("counts", counts, "int32", (E + 1,))
+    _dense("dtopk_w", dtopk_w, "float32", (T, k))
+    _dense("dloss", dloss, "float32", (2,))
+    _dense("dlogits", dlogits, "float32", (T, E))
+    _check(lib.bqm_router_grad(_ptr(logits), _ptr(topk_idx), _ptr(valid), _ptr(counts), _ptr(dtopk_w), _ptr(dloss), T,
+                               E, k, int(renorm), _ptr(dlogits), _stream(stream)))
+    return dlogits

@@ -1,4 +1,4 @@
-// NVFP4 (Four-Over-Six) and NF4 quantizers and dequantizers for gfx950.
+// NVFP4 (Four-Over-Six), NF4 and MXFP4 quantizers and dequantizers for gfx950.
 //
 // NVFP4: one E4M3 scale per 16 consecutive elements along the last axis and
 // one FP32 scale per 2-D matrix (weights) or per row (token activations); each
@@ -586,6 +586,109 @@ __global__ void __launch_bounds__(kThreads) nf4_dequant(const uint32_t *__restri
   }
 }
 
+// ---------------------------------------------------------------------------
+// MXFP4: blocks of 32 elements along cols, one E8M0 scale byte per block
+// ---------------------------------------------------------------------------
+// With A = max|x| of the block, the scale is 2^(floor(log2 A) - 2) (2 is the exponent
+// of E2M1's largest value), held as its exponent plus 127 and clamped to [0, 254]; a
+// zero block has code 0.  Each element is x 2^-s rounded to the nearest E2M1 value,
+// ties to even, saturating at 6.  A block that holds an infinity or NaN gets scale
+// 255 (E8M0's NaN) and codes 0, and decodes to NaN.
+//
+// Bound by HBM: 2.53 bytes per element in each direction.  One lane per 8 elements as
+// in the kernels above, so a quad of lanes shares a block: its maximum is two
+// quad-permute moves, with no LDS and no barrier.
+constexpr uint32_t kE8M0NaN = 255u;
+
+// maximum over the four lanes of a quad
+__device__ __forceinline__ uint32_t quad_max_u(uint32_t v) {
+  uint32_t t = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false);  // quad_perm 1,0,3,2
+  v = v > t ? v : t;
+  t = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false);  // quad_perm 2,3,0,1
+  return v > t ? v : t;
+}
+
+// one code word (8 elements) of a block whose largest |x| has the bf16 bits mx; sets
+// the block's scale code.  x 2^-s is exact in FP32 (a power of two; bf16 subnormals
+// become normal, as s is clamped at -127), so the conversion's rounding is the only one.
+__device__ __forceinline__ uint32_t mxfp4_word(const uint32_t (&w)[4], uint32_t mx, uint32_t &sc) {
+  if (mx >= 0x7F80u) {
+    sc = kE8M0NaN;
+    return 0u;
+  }
+  const uint32_t ex = mx >> 7;      // biased exponent of A (0 for zero and subnormals)
+  sc = ex > 2u ? ex - 2u : 0u;      // floor(log2 A) - 2 + 127
+  const float r = __uint_as_float((254u - sc) << 23);  // 2^-s, s = sc - 127
+  uint32_t c = 0u;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, bf16_lo(w[0]) * r, bf16_hi(w[0]) * r, 1.0f, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, bf16_lo(w[1]) * r, bf16_hi(w[1]) * r, 1.0f, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, bf16_lo(w[2]) * r, bf16_hi(w[2]) * r, 1.0f, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, bf16_lo(w[3]) * r, bf16_hi(w[3]) * r, 1.0f, 3);
+  return c;
+}
+
+__global__ void __launch_bounds__(kThreads) mxfp4_quant(const uint4 *__restrict__ x, int64_t nunits,
+                                                        uint32_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+  const int64_t base = (int64_t)blockIdx.x * kDqUnits;
+  uint4 v[kDqIter];
+#pragma unroll
+  for (int it = 0; it < kDqIter; ++it) {
+    const int64_t u0 = base + it * kThreads + threadIdx.x;
+    v[it] = ld_nt(&x[u0 < nunits ? u0 : nunits - 1]);
+  }
+#pragma unroll
+  for (int it = 0; it < kDqIter; ++it) {
+    const int64_t u = base + it * kThreads + threadIdx.x;
+    const uint32_t w[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
+    uint32_t mx = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t m = absmax_bits_u32(w[i]);
+      mx = mx > m ? mx : m;
+    }
+    mx = quad_max_u(mx);  // nunits is a multiple of 4: a quad is in range or out as one
+    uint32_t sc;
+    const uint32_t c = mxfp4_word(w, mx, sc);
+    if (u < nunits) {
+      __builtin_nontemporal_store(c, &codes[u]);
+      if ((threadIdx.x & 3) == 0) __builtin_nontemporal_store((uint8_t)sc, &scales[u >> 2]);
+    }
+  }
+}
+
+// byte P of a code word -> bf16 pair, v 2^s (exact: E2M1 has two significant bits, and
+// the least nonzero magnitude 2^-128 is a bf16 subnormal)
+template <int P>
+__device__ __forceinline__ uint32_t mxfp4_dq_pair(uint32_t c, float sc) {
+  const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, P);
+  return pack_bf16_rne(v.x * sc, v.y * sc);
+}
+
+__global__ void __launch_bounds__(kThreads) mxfp4_dequant(const uint32_t *__restrict__ codes,
+                                                          const uint8_t *__restrict__ scales, int64_t nunits,
+                                                          uint4 *__restrict__ y) {
+  const int64_t base = (int64_t)blockIdx.x * kDqUnits;
+  uint32_t c[kDqIter], sb[kDqIter];
+#pragma unroll
+  for (int it = 0; it < kDqIter; ++it) {
+    const int64_t u0 = base + it * kThreads + threadIdx.x;
+    const int64_t u = u0 < nunits ? u0 : nunits - 1;
+    c[it] = codes[u];
+    sb[it] = scales[u >> 2];
+  }
+#pragma unroll
+  for (int it = 0; it < kDqIter; ++it) {
+    const int64_t u = base + it * kThreads + threadIdx.x;
+    if (u < nunits) {
+      // 2^(sb - 127): a normal float from sb = 1 on, the subnormal 2^-127 for sb = 0
+      const float sc = sb[it] == kE8M0NaN ? __uint_as_float(0x7FC00000u)
+                                          : __uint_as_float(sb[it] ? sb[it] << 23 : 0x00400000u);
+      st_nt(&y[u], make_uint4(mxfp4_dq_pair<0>(c[it], sc), mxfp4_dq_pair<1>(c[it], sc), mxfp4_dq_pair<2>(c[it], sc),
+                              mxfp4_dq_pair<3>(c[it], sc)));
+    }
+  }
+}
+
 // Nested absmax, pass 1: one workgroup of 1024 threads per matrix of nb blocks, and
 // offset = fl32(fl64(sum) / nb) to sd[m (1 + G)], where fl64(sum) is the exact sum of
 // the matrix's FP32 absmax rounded once to the nearest double (ties to even), so the
@@ -743,13 +846,13 @@ int grid_for(int64_t work_items, int per_block = kThreads, int cap = 65536) {
 
 bqm_status check_qtensor(const bqm_qtensor *q, const char *who, bool need_sdec) {
   BQM_REQUIRE(q, BQM_ERR_INVALID_ARG, "%s: qtensor is NULL", who);
-  BQM_REQUIRE(q->fmt == BQM_FMT_NVFP4 || q->fmt == BQM_FMT_NF4, BQM_ERR_INVALID_ARG,
+  BQM_REQUIRE(q->fmt == BQM_FMT_NVFP4 || q->fmt == BQM_FMT_NF4 || q->fmt == BQM_FMT_MXFP4, BQM_ERR_INVALID_ARG,
               "%s: unknown format %d", who, q->fmt);
   BQM_REQUIRE(q->n_mat >= 0 && q->rows >= 0 && q->cols >= 0, BQM_ERR_INVALID_ARG,
               "%s: negative size", who);
   BQM_REQUIRE(q->nested == 0 || (q->fmt == BQM_FMT_NF4 && q->nested == 1), BQM_ERR_INVALID_ARG,
               "%s: nested must be 0, or 1 for NF4", who);
-  int64_t blk = q->fmt == BQM_FMT_NVFP4 ? 16 : 64;
+  int64_t blk = q->fmt == BQM_FMT_NVFP4 ? 16 : (q->fmt == BQM_FMT_MXFP4 ? 32 : 64);
   BQM_REQUIRE(q->cols % blk == 0, BQM_ERR_SHAPE, "%s: cols=%lld is not a multiple of %lld", who,
               (long long)q->cols, (long long)blk);
   int64_t n = q->n_mat * q->rows * q->cols;
@@ -960,6 +1063,21 @@ extern "C" bqm_status bqm_quantize_nf4(const uint16_t *x, bqm_qtensor *out, void
   return launch_status("nf4_quant");
 }
 
+extern "C" bqm_status bqm_quantize_mxfp4(const uint16_t *x, bqm_qtensor *out, void *stream) {
+  bqm_status st = check_qtensor(out, "bqm_quantize_mxfp4", false);
+  if (st != BQM_OK) return st;
+  BQM_REQUIRE(out->fmt == BQM_FMT_MXFP4, BQM_ERR_INVALID_ARG, "bqm_quantize_mxfp4: out->fmt must be BQM_FMT_MXFP4");
+  const int64_t n = out->n_mat * out->rows * out->cols;
+  if (n == 0) return BQM_OK;
+  BQM_REQUIRE(x, BQM_ERR_INVALID_ARG, "bqm_quantize_mxfp4: x is NULL");
+  BQM_REQUIRE(aligned16(x), BQM_ERR_ALIGN, "bqm_quantize_mxfp4: x not 16-byte aligned");
+  BQM_REQUIRE(n / 8 / kDqUnits < INT32_MAX, BQM_ERR_SHAPE, "bqm_quantize_mxfp4: tensor too large");
+  mxfp4_quant<<<dq_grid(n), kThreads, 0, as_stream(stream)>>>(
+      reinterpret_cast<const uint4 *>(x), n / 8, reinterpret_cast<uint32_t *>(out->codes),
+      reinterpret_cast<uint8_t *>(out->scales));
+  return launch_status("mxfp4_quant");
+}
+
 extern "C" bqm_status bqm_dequantize(const bqm_qtensor *q, uint16_t *y, void *stream) {
   bqm_status st = check_qtensor(q, "bqm_dequantize", true);
   if (st != BQM_OK) return st;
@@ -976,6 +1094,12 @@ extern "C" bqm_status bqm_dequantize(const bqm_qtensor *q, uint16_t *y, void *st
         reinterpret_cast<const uint32_t *>(q->codes), reinterpret_cast<const uint8_t *>(q->scales), q->s_dec,
         n / 8, seg_units, reinterpret_cast<uint4 *>(y));
     return launch_status("nvfp4_dequant");
+  }
+  if (q->fmt == BQM_FMT_MXFP4) {
+    mxfp4_dequant<<<dq_grid(n), kThreads, 0, s>>>(reinterpret_cast<const uint32_t *>(q->codes),
+                                                  reinterpret_cast<const uint8_t *>(q->scales), n / 8,
+                                                  reinterpret_cast<uint4 *>(y));
+    return launch_status("mxfp4_dequant");
   }
   const int64_t nb = q->rows * q->cols / 64;
   if (q->nested)

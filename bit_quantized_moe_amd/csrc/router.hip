@@ -1,0 +1,497 @@
+// The router's training: balance loss, z-loss and per-expert counts, and the gradient of
+// the logits through the losses and the routing weights.
+//
+// Over the n tokens that count (valid[t] != 0), with p_t = softmax(l_t), c_e the routed
+// pairs of expert e, f_e = c_e / (n k) and P_e = mean_t p_te:
+//   L_b = E sum_e f_e P_e,    L_z = mean_t lse(l_t)^2.
+// Gradient (the counts are constants), with g_b, g_z the losses' gradients, q_j = p_{t,i_j}:
+//   G_e = g_b E f_e / n + sum_{j: i_j = e} dq_j,
+//   dl_te = p_te (G_e - sum_e' p_te' G_e') + (2 g_z / n) lse_t p_te,
+// where dq_j = dw_j, or, with weights w_j = q_j / S, S = sum_j q_j,
+// dq_j = (dw_j - sum_m w_m dw_m) / S.  In that second case the routing weights' share of
+// sum_e p_e G_e is zero, and their term is p_e (A_e - D m_e) / S with A_e = sum of dw_j
+// over j with i_j = e, m_e their number, D = sum_e p_e A_e / S.
+//
+// Bound by HBM: each direction reads the T E logits once (the softmax is recomputed from
+// registers in the backward rather than kept, which would cost a write and a read of the
+// same size); the gradient is written once.  A token is held by 2^n lanes, 4 NV logits a
+// lane, so a row is read with 16-byte loads and all its sums are moves between lanes.
+#include "common.h"
+
+#include <type_traits>
+
+namespace bqm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kMaxE = 1024, kMaxK = 16;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// Reductions over groups of L lanes (a power of two); every lane gets the result.  Within
+// 16 lanes by DPP moves, beyond that by cross-lane shuffles.
+template <int L, class F>
+__device__ __forceinline__ float group_reduce(float v, F op) {
+  if constexpr (L >= 2) v = op(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, false)));
+  if constexpr (L >= 4) v = op(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, false)));
+  if constexpr (L >= 8) v = op(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, false)));
+  if constexpr (L >= 16) v = op(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, false)));
+  if constexpr (L >= 32) v = op(v, __shfl_xor(v, 16, 64));
+  if constexpr (L >= 64) v = op(v, __shfl_xor(v, 32, 64));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+  return group_reduce<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
+  return group_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// e^x for x <= 0 within about an ulp: 2^(x log2 e) with the rounding of the product put back
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLo = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
+  const float t = x * kLog2e;
+  if (x < -104.0f) return 0.0f;  // also -inf, where the correction below would be NaN
+  const float r = __builtin_fmaf(x, kLog2eLo, __builtin_fmaf(x, kLog2e, -t));
+  const float y = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(y, r * kLn2, y);
+}
+
+// A token's logits in its group's registers: slot (v, c) of lane l is expert
+// 4 (v L + l) + c with 16-byte loads (E % 4 == 0), else (4 v + c) L + l.
+template <int L, int NV, bool VEC>
+__device__ __forceinline__ int expert_of(int v, int c, int l) {
+  return VEC ? 4 * (v * L + l) + c : (4 * v + c) * L + l;
+}
+
+template <int L, int NV, bool VEC>
+__device__ __forceinline__ void load_row(const float *__restrict__ row, int E, int l, bool use, f32x4 (&x)[NV]) {
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if constexpr (VEC) {
+      const int e = expert_of<L, NV, VEC>(v, 0, l);
+      x[v] = use && e < E ? *reinterpret_cast<const f32x4 *>(row + e)
+                          : f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int e = expert_of<L, NV, VEC>(v, c, l);
+        x[v][c] = use && e < E ? row[e] : -INFINITY;
+      }
+    }
+  }
+}
+
+// x <- e^(x - max); returns 1 / sum (0 for a row of nothing but -inf) and the row's lse
+// (0 for such a row)
+template <int L, int NV>
+__device__ __forceinline__ float softmax_row(f32x4 (&x)[NV], float &lse) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) m = fmaxf(m, fmaxf(fmaxf(x[v][0], x[v][1]), fmaxf(x[v][2], x[v][3])));
+  m = group_max<L>(m);
+  const float base = m == -INFINITY ? 0.0f : m;
+  float s = 0.0f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      x[v][c] = exp_neg(x[v][c] - base);
+      s += x[v][c];
+    }
+  s = group_sum<L>(s);
+  lse = m == -INFINITY ? 0.0f : m + logf(s);
+  return s > 0.0f ? 1.0f / s : 0.0f;
+}
+
+// ---------------------------------------------------------------------------
+// losses and counts
+// ---------------------------------------------------------------------------
+// Workspace: per workgroup of the first kernel, E sums of p (FP32), E counts and the sum
+// of lse^2 and the tokens that count; then the finishing kernel's partial losses and its
+// arrival counter.
+struct LossWs {
+  float *psum;        // [G][E]
+  int32_t *counts;    // [G][E]
+  float *z;           // [G]
+  int32_t *n;         // [G]
+  double *part;       // [kMaxE / kFinE]
+  uint32_t *arrived;  // 1
+};
+
+constexpr int kFinE = 32;  // experts per workgroup of the finishing kernel
+
+struct LossGeom {
+  int G;        // workgroups of the first kernel
+  size_t bytes;
+};
+
+// Tokens per workgroup at least kTokMin, so that a small batch writes few partial sums;
+// at most 512 workgroups (two of 4 waves per CU keep the row loads in flight).
+constexpr int64_t kTokMin = 32;
+LossGeom loss_geom(int64_t T, int32_t E) {
+  int64_t G = cdiv(T, kTokMin);
+  G = G < 1 ? 1 : (G > 512 ? 512 : G);
+  LossGeom g;
+  g.G = (int)G;
+  g.bytes = align256((size_t)G * E * 4) * 2 + align256((size_t)G * 4) * 2 + align256(kMaxE / kFinE * sizeof(double)) + 256;
+  return g;
+}
+
+LossWs loss_ws(void *ws, int G, int E) {
+  LossWs w;
+  char *p = reinterpret_cast<char *>(ws);
+  w.psum = reinterpret_cast<float *>(p);
+  p += align256((size_t)G * E * 4);
+  w.counts = reinterpret_cast<int32_t *>(p);
+  p += align256((size_t)G * E * 4);
+  w.z = reinterpret_cast<float *>(p);
+  p += align256((size_t)G * 4);
+  w.n = reinterpret_cast<int32_t *>(p);
+  p += align256((size_t)G * 4);
+  w.part = reinterpret_cast<double *>(p);
+  p += align256(kMaxE / kFinE * sizeof(double));
+  w.arrived = reinterpret_cast<uint32_t *>(p);
+  return w;
+}
+
+template <int L, int NV, bool VEC>
+__global__ void __launch_bounds__(kThreads) router_sums(const float *__restrict__ logits,
+                                                        const int32_t *__restrict__ idx,
+                                                        const uint8_t *__restrict__ valid, int64_t T, int E, int k,
+                                                        LossWs w) {
+  constexpr int kGroups = kThreads / L;
+  __shared__ float ps[kMaxE];
+  __shared__ int32_t hist[kMaxE];
+  __shared__ float zs[kWaves];
+  __shared__ int32_t ns[kWaves];
+  const int tid = threadIdx.x, l = tid & (L - 1), grp = tid / L, wave = tid >> 6, lane = tid & 63;
+  for (int e = tid; e < E; e += kThreads) {
+    ps[e] = 0.0f;
+    hist[e] = 0;
+  }
+  if (blockIdx.x == 0 && tid == 0) *w.arrived = 0u;
+  __syncthreads();
+  f32x4 acc[NV] = {};
+  float z = 0.0f;
+  int32_t n = 0;
+  for (int64_t t = (int64_t)blockIdx.x * kGroups + grp; t < T; t += (int64_t)gridDim.x * kGroups) {
+    const bool use = !valid || valid[t];
+    f32x4 x[NV];
+    load_row<L, NV, VEC>(logits + t * E, E, l, use, x);
+    if (use)
+      for (int j = l; j < k; j += L) {
+        const int e = idx[t * k + j];
+        if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
+      }
+    float lse;
+    const float inv = softmax_row<L, NV>(x, lse);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) acc[v] += x[v] * inv;
+    if (use && l == 0) {
+      z += lse * lse;
+      ++n;
+    }
+  }
+  // the groups of a wave added in a fixed butterfly, the waves in wave order
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int m = L; m < 64; m <<= 1) acc[v][c] += __shfl_xor(acc[v][c], m, 64);
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    z += __shfl_xor(z, m, 64);
+    n += __shfl_xor(n, m, 64);
+  }
+  if (lane == 0) {
+    zs[wave] = z;
+    ns[wave] = n;
+  }
+  for (int q = 0; q < kWaves; ++q) {
+    if (wave == q && lane < L) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int e = expert_of<L, NV, VEC>(v, c, l);
+          if (e < E) ps[e] += acc[v][c];
+        }
+    }
+    __syncthreads();
+  }
+  for (int e = tid; e < E; e += kThreads) {
+    w.psum[(int64_t)blockIdx.x * E + e] = ps[e];
+    w.counts[(int64_t)blockIdx.x * E + e] = hist[e];
+  }
+  if (tid == 0) {
+    float zt = 0.0f;
+    int32_t nt = 0;
+    for (int q = 0; q < kWaves; ++q) {
+      zt += zs[q];
+      nt += ns[q];
+    }
+    w.z[blockIdx.x] = zt;
+    w.n[blockIdx.x] = nt;
+  }
+}
+
+// Workgroup b adds the G partial sums of experts kFinE b .. in FP64 and forms their share
+// sum_e c_e P_e; the workgroup that arrives last adds the shares in order.  (The counter is
+// cleared by the first kernel of the same call, so a workspace needs no preparation.)
+constexpr int kFinParts = kThreads / kFinE;
+
+__global__ void __launch_bounds__(kThreads) router_finish(LossWs w, int G, int E, int k, int32_t *__restrict__ counts,
+                                                          float *__restrict__ loss) {
+  __shared__ double ps[kFinParts][kFinE];
+  __shared__ int32_t cs[kFinParts][kFinE];
+  __shared__ uint32_t rank;
+  const int tid = threadIdx.x, el = tid % kFinE, part = tid / kFinE;
+  const int e = blockIdx.x * kFinE + el;
+  double p = 0.0;
+  int32_t c = 0;
+  if (e < E)
+    for (int g = part; g < G; g += kFinParts) {
+      p += (double)w.psum[(int64_t)g * E + e];
+      c += w.counts[(int64_t)g * E + e];
+    }
+  ps[part][el] = p;
+  cs[part][el] = c;
+  __syncthreads();
+  if (tid < kFinE) {
+    p = 0.0;
+    c = 0;
+    for (int q = 0; q < kFinParts; ++q) {
+      p += ps[q][el];
+      c += cs[q][el];
+    }
+    if (e < E) counts[e] = c;
+    ps[0][el] = (double)c * p;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    double s = 0.0;
+    for (int q = 0; q < kFinE; ++q) s += ps[0][q];
+    __hip_atomic_store(&w.part[blockIdx.x], s, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
+    rank = __hip_atomic_fetch_add(w.arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (rank != gridDim.x - 1) return;
+  // the last workgroup: tokens and lse^2 over the G partial sums, then the losses
+  double z = 0.0;
+  int32_t n = 0;
+  for (int g = tid; g < G; g += kThreads) {
+    z += (double)w.z[g];
+    n += w.n[g];
+  }
+  double *zs = &ps[0][0];
+  int32_t *ns = &cs[0][0];
+  zs[tid] = z;
+  ns[tid] = n;
+  __syncthreads();
+  for (int s = kThreads / 2; s > 0; s >>= 1) {
+    if (tid < s) {
+      zs[tid] += zs[tid + s];
+      ns[tid] += ns[tid + s];
+    }
+    __syncthreads();
+  }
+  if (tid == 0) {
+    double b = 0.0;
+    for (unsigned q = 0; q < gridDim.x; ++q)
+      b += __hip_atomic_load(&w.part[q], __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_AGENT);
+    const double nn = (double)ns[0];
+    counts[E] = ns[0];
+    loss[0] = ns[0] > 0 ? (float)((double)E * b / (nn * nn * (double)k)) : 0.0f;
+    loss[1] = ns[0] > 0 ? (float)(zs[0] / nn) : 0.0f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// gradient of the logits
+// ---------------------------------------------------------------------------
+template <int L, int NV, bool VEC>
+__global__ void __launch_bounds__(kThreads) router_grad(const float *__restrict__ logits,
+                                                        const int32_t *__restrict__ idx,
+                                                        const uint8_t *__restrict__ valid,
+                                                        const int32_t *__restrict__ counts,
+                                                        const float *__restrict__ dw, const float *__restrict__ dloss,
+                                                        int64_t T, int E, int k, int renorm,
+                                                        float *__restrict__ dlogits) {
+  constexpr int kGroups = kThreads / L;
+  const int tid = threadIdx.x, l = tid & (L - 1), grp = tid / L;
+  // the losses' gradients per expert: g_b E f_e / n, and 2 g_z / n
+  const int32_t n = counts[E];
+  const float rn = n > 0 ? 1.0f / (float)n : 0.0f;
+  const float gz = dloss ? 2.0f * dloss[1] * rn : 0.0f;
+  const float gb = dloss ? dloss[0] * rn * rn * (float)E / (float)k : 0.0f;
+  f32x4 fe[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int e = expert_of<L, NV, VEC>(v, c, l);
+      fe[v][c] = e < E ? gb * (float)counts[e] : 0.0f;
+    }
+  for (int64_t t = (int64_t)blockIdx.x * kGroups + grp; t < T; t += (int64_t)gridDim.x * kGroups) {
+    const bool use = !valid || valid[t];
+    f32x4 x[NV];
+    load_row<L, NV, VEC>(logits + t * E, E, l, use, x);
+    // A_e and, for renormalised weights, m_e
+    f32x4 a[NV] = {}, m[NV] = {};
+    if (dw && use)
+      for (int j = 0; j < k; ++j) {
+        const int i = idx[t * k + j];
+        const float d = dw[t * k + j];
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const bool hit = i == expert_of<L, NV, VEC>(v, c, l);
+            a[v][c] += hit ? d : 0.0f;
+            if (renorm) m[v][c] += hit ? 1.0f : 0.0f;
+          }
+      }
+    float lse;
+    const float inv = softmax_row<L, NV>(x, lse);
+    float sf = 0.0f, sa = 0.0f, sm = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      x[v] *= inv;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        sf += x[v][c] * fe[v][c];
+        sa += x[v][c] * a[v][c];
+        if (renorm) sm += x[v][c] * m[v][c];
+      }
+    }
+    sf = group_sum<L>(sf);
+    sa = group_sum<L>(sa);
+    float dm = 0.0f, rs = 1.0f, off = sa;  // routing weights: p (rs (A - dm m) - off)
+    if (renorm) {
+      sm = group_sum<L>(sm);
+      rs = sm > 0.0f ? 1.0f / sm : 0.0f;
+      dm = sa * rs;
+      off = 0.0f;
+    }
+    const float shift = gz * lse - sf - off;
+    float *out = dlogits + t * E;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      f32x4 g;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float q = a[v][c];
+        if (renorm) q = (q - dm * m[v][c]) * rs;
+        g[c] = x[v][c] * (fe[v][c] + q + shift);
+      }
+      if constexpr (VEC) {
+        const int e = expert_of<L, NV, VEC>(v, 0, l);
+        if (e < E) *reinterpret_cast<f32x4 *>(out + e) = g;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int e = expert_of<L, NV, VEC>(v, c, l);
+          if (e < E) out[e] = g[c];
+        }
+      }
+    }
+  }
+}
+
+bqm_status check_router(const char *who, int64_t T, int32_t E, int32_t k) {
+  BQM_REQUIRE(T >= 0, BQM_ERR_INVALID_ARG, "%s: T < 0", who);
+  BQM_REQUIRE(E >= 1 && E <= kMaxE, BQM_ERR_SHAPE, "%s: E=%d outside [1, 1024]", who, E);
+  BQM_REQUIRE(k >= 1 && k <= E && k <= kMaxK, BQM_ERR_SHAPE, "%s: k=%d outside [1, min(E,16)]", who, k);
+  // per-expert counts are 32-bit
+  BQM_REQUIRE(T * k < ((int64_t)1 << 31), BQM_ERR_SHAPE, "%s: T*k too large", who);
+  return BQM_OK;
+}
+
+// Calls f with the lanes per token, the 4-logit vectors per lane and the load form for E.
+// Four logits a lane up to 256 experts: the lanes per token halve with E, so a wave takes
+// several tokens of a small router.
+template <class F>
+void with_shape(int E, F f) {
+  auto vec = [&](auto L, auto NV) {
+    if (E % 4 == 0)
+      f(L, NV, std::true_type{});
+    else
+      f(L, NV, std::false_type{});
+  };
+  using std::integral_constant;
+  if (E <= 16)
+    vec(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  else if (E <= 32)
+    vec(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  else if (E <= 64)
+    vec(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  else if (E <= 128)
+    vec(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  else if (E <= 256)
+    vec(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (E <= 512)
+    vec(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else
+    vec(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+}
+
+}  // namespace
+}  // namespace bqm
+
+using namespace bqm;
+
+extern "C" size_t bqm_router_loss_workspace_size(int64_t T, int32_t E) {
+  if (T < 0 || E < 1 || E > kMaxE) return 0;
+  return loss_geom(T, E).bytes;
+}
+
+extern "C" bqm_status bqm_router_loss(const float *logits, const int32_t *topk_idx, const uint8_t *valid, int64_t T,
+                                      int32_t E, int32_t k, int32_t *counts, float *loss, void *ws, size_t ws_bytes,
+                                      void *stream) {
+  const char *who = "bqm_router_loss";
+  bqm_status st = check_router(who, T, E, k);
+  if (st != BQM_OK) return st;
+  BQM_REQUIRE(counts && loss, BQM_ERR_INVALID_ARG, "%s: counts or loss is NULL", who);
+  BQM_REQUIRE(T == 0 || (logits && topk_idx), BQM_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  BQM_REQUIRE(aligned16(logits) && aligned16(topk_idx) && aligned16(valid) && aligned16(counts) && aligned16(loss),
+              BQM_ERR_ALIGN, "%s: pointer not 16-byte aligned", who);
+  const LossGeom g = loss_geom(T, E);
+  BQM_REQUIRE(ws && ws_bytes >= g.bytes, BQM_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", who,
+              g.bytes, ws_bytes);
+  BQM_REQUIRE(aligned16(ws), BQM_ERR_ALIGN, "%s: ws not 16-byte aligned", who);
+  const LossWs w = loss_ws(ws, g.G, E);
+  hipStream_t s = as_stream(stream);
+  with_shape(E, [&](auto L, auto NV, auto VEC) {
+    router_sums<L.value, NV.value, VEC.value><<<g.G, kThreads, 0, s>>>(logits, topk_idx, valid, T, E, k, w);
+  });
+  st = launch_status("router_sums");
+  if (st != BQM_OK) return st;
+  router_finish<<<(unsigned)cdiv(E, kFinE), kThreads, 0, s>>>(w, g.G, E, k, counts, loss);
+  return launch_status("router_finish");
+}
+
+extern "C" bqm_status bqm_router_grad(const float *logits, const int32_t *topk_idx, const uint8_t *valid,
+                                      const int32_t *counts, const float *dtopk_w, const float *dloss, int64_t T,
+                                      int32_t E, int32_t k, int32_t renorm, float *dlogits, void *stream) {
+  const char *who = "bqm_router_grad";
+  bqm_status st = check_router(who, T, E, k);
+  if (st != BQM_OK) return st;
+  if (T == 0) return BQM_OK;
+  BQM_REQUIRE(logits && topk_idx && counts && dlogits, BQM_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  BQM_REQUIRE(aligned16(logits) && aligned16(topk_idx) && aligned16(valid) && aligned16(counts) &&
+                  aligned16(dtopk_w) && aligned16(dloss) && aligned16(dlogits),
+              BQM_ERR_ALIGN, "%s: pointer not 16-byte aligned", who);
+  with_shape(E, [&](auto L, auto NV, auto VEC) {
+    constexpr int kGroups = kThreads / L.value;
+    const int64_t G = cdiv(T, kGroups);
+    const unsigned grid = (unsigned)(G < 2048 ? G : 2048);
+    router_grad<L.value, NV.value, VEC.value><<<grid, kThreads, 0, as_stream(stream)>>>(
+        logits, topk_idx, valid, counts, dtopk_w, dloss, T, E, k, renorm, dlogits);
+  });
+  return launch_status("router_grad");
+}

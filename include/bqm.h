@@ -46,7 +46,7 @@ typedef enum {
   BQM_ERR_HIP = -6          /* a HIP launch or runtime error */
 } bqm_status;
 
-typedef enum { BQM_FMT_NVFP4 = 1, BQM_FMT_NF4 = 2 } bqm_format;
+typedef enum { BQM_FMT_NVFP4 = 1, BQM_FMT_NF4 = 2, BQM_FMT_MXFP4 = 3 } bqm_format;
 typedef enum { BQM_SCALE_PER_TENSOR = 0, BQM_SCALE_PER_ROW = 1 } bqm_scale_mode;
 
 /* A rowwise-quantized stack [n_mat, rows, cols]; blocks run along cols (the
@@ -54,14 +54,15 @@ typedef enum { BQM_SCALE_PER_TENSOR = 0, BQM_SCALE_PER_ROW = 1 } bqm_scale_mode;
  * "The 4-bit base that was actually using 8-bit memory": the columnwise copy is
  * dropped and the backward reads this one transposed).
  *   codes : uint8 [n_mat, rows, cols/2]; element 2j is the low nibble of byte j,
- *           element 2j+1 the high nibble.  NVFP4: E2M1 with the sign in bit 3.
+ *           element 2j+1 the high nibble.  NVFP4, MXFP4: E2M1 with the sign in bit 3.
  *           NF4: index 0..15 into the NormalFloat codebook.
  *   scales: NVFP4: uint8 E4M3FN bits [n_mat, rows, cols/16];
  *           NF4: float absmax [n_mat, rows, cols/64];
- *           NF4 nested: uint8 E4M3FN bits [n_mat, rows, cols/64] (see below).
+ *           NF4 nested: uint8 E4M3FN bits [n_mat, rows, cols/64] (see below);
+ *           MXFP4: uint8 E8M0 codes [n_mat, rows, cols/32], 2^(code - 127), 255 = NaN.
  *   s_dec : NVFP4: float [n_mat] (per tensor) or [n_mat*rows] (per row);
  *           the value of an element is e2m1(code) * e4m3(scale) * s_dec.
- *           NF4: NULL.  NF4 nested: float [n_mat, 1 + G], G = ceil(rows*cols/64/256):
+ *           NF4, MXFP4: NULL (scale_mode is not read).  NF4 nested: float [n_mat, 1 + G], G = ceil(rows*cols/64/256):
  *           per matrix the offset, then the scale of each group of 256 blocks.
  *   four_over_six: the mode the stack was quantized with (metadata).
  *   nested: NF4 only.  1: the absmax is double-quantized (the nested code of
@@ -156,6 +157,14 @@ bqm_status bqm_quantize_nf4(const uint16_t *x, bqm_qtensor *out /* host struct *
  * not depend on the order of the additions; at most 2^31 blocks per matrix. */
 bqm_status bqm_nf4_nest(const bqm_qtensor *plain, bqm_qtensor *nested, void *stream);
 
+/* MXFP4 quantization (the OCP microscaling format): blocks of 32 along cols, one
+ * power-of-two scale 2^s per block, s = floor(log2(max|x|)) - 2 (2 is the exponent of
+ * E2M1's largest value) clamped to [-127, 127], and E2M1 codes of x 2^-s rounded to
+ * nearest even, saturating at 6.  A zero block gets scale code 0; a block that holds
+ * an infinity or NaN gets scale code 255 and codes 0, and decodes to NaN.
+ * x: bf16 [n_mat, rows, cols], cols % 32 == 0; out->fmt == BQM_FMT_MXFP4. */
+bqm_status bqm_quantize_mxfp4(const uint16_t *x, bqm_qtensor *out /* host struct */, void *stream);
+
 /* Dequantize a stack to bf16 [n_mat, rows, cols] (the DQ of DQ(Q(W)): GLM page,
  * section "The 4-bit base that was actually using 8-bit memory", where the one
  * rowwise copy is dequantized to bf16 for the backward; 4-bitter page, section
@@ -163,7 +172,9 @@ bqm_status bqm_nf4_nest(const bqm_qtensor *plain, bqm_qtensor *nested, void *str
  * nf4moe page, section "The fix: dequant-on-forward for routed experts", for NF4):
  *   NVFP4: bf16_rne(fl32(e2m1(code) * e4m3(scale)) * s_dec)  (one FP32 rounding)
  *   NF4:   bf16_rne(fl32(level[code] * absmax)), absmax' when nested
- * q: a stack as bqm_quantize_nvfp4 / bqm_quantize_nf4 / bqm_nf4_nest wrote it
+ *   MXFP4: e2m1(code) * 2^(scale - 127), exact in bf16; NaN for scale code 255
+ * q: a stack as bqm_quantize_nvfp4 / bqm_quantize_nf4 / bqm_nf4_nest /
+ * bqm_quantize_mxfp4 wrote it
  * (read only); y: bf16 [n_mat, rows, cols], written.  Errors: a bad format, a
  * NULL or unaligned pointer, or cols not a multiple of the block size.
  * The same values (without the s_dec factor, which the GEMMs apply to their
@@ -193,6 +204,87 @@ bqm_status bqm_route(const float *logits, int64_t T, int32_t E, int32_t k, int32
 size_t bqm_permute_workspace_size(int64_t T, int32_t E, int32_t k);
 bqm_status bqm_permute(const int32_t *topk_idx, int64_t T, int32_t E, int32_t k, int32_t *perm,
                        int32_t *inv, int32_t *offsets, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Experts over MXFP4: the two products of an expert layer whose frozen weights and
+ * activations are MXFP4, the SwiGLU between them with an 8-bit copy of its input for
+ * the backward, and the router's training.  Rows are the routed pairs in expert order
+ * as bqm_permute gives them.  One layer, forward and backward:
+ *   bqm_route, bqm_permute, bqm_router_loss; bqm_quantize_mxfp4 (x);
+ *   bqm_mxfp4_gemm (x, w_gu, perm) -> h; bqm_swiglu_ckpt_fwd (h) -> checkpoint, a in
+ *   MXFP4; bqm_mxfp4_gemm (a, w_dn, no perm) -> the routed rows y, combined per token;
+ *   bqm_mxfp4_dgrad (w_dn, dy, perm) -> da; bqm_swiglu_ckpt_bwd -> dh, dtopk_w;
+ *   bqm_mxfp4_dgrad (w_gu, dh, no perm) -> the rows of dx; bqm_router_grad -> dlogits.
+ * The activation quantizers are the identity in the backward, as in the layer below. */
+
+/* Grouped product y[pos, n] = sum_k X[row, k] W[e, n, k], rounded to bf16 once, for
+ * offsets[e] <= pos < offsets[e + 1], row = perm[pos] / k with perm, pos without.
+ * x: MXFP4 [1, rows, K]; w: MXFP4 [E, N, K]; N % 32 == 0, K % 32 == 0, E <= 1024;
+ * offsets i32 [E+1]; perm i32 [R] or NULL; R = rows * k with perm, rows without (k is
+ * then not read); y bf16 [R, N].  The products of the 4-bit values are exact, sums are
+ * FP32.  Rows that belong to no expert (from offsets[E] on) are left as they were; only
+ * experts with rows are read.  Offsets are clamped to [0, R] and source rows to [0, rows)
+ * where they are read, so that no value in them reaches memory outside the tensors.
+ * Results do not depend on the other rows of the batch beyond the order of the FP32
+ * sums, which goes by R / E. */
+bqm_status bqm_mxfp4_gemm(const bqm_qtensor *x /* host struct */, const bqm_qtensor *w /* host struct */,
+                          const int32_t *offsets, const int32_t *perm, int32_t k, int64_t R, uint16_t *y,
+                          void *stream);
+
+/* Its input gradient dx[pos, k] = sum_n dY[row, n] DQ(W)[e, n, k] over the same rowwise
+ * copy: dy bf16 [dy_rows, N], dx bf16 [R, K]; the rest as for bqm_mxfp4_gemm (R =
+ * dy_rows * k with perm, dy_rows without).  dY is not quantized; sums are FP32. */
+bqm_status bqm_mxfp4_dgrad(const bqm_qtensor *w /* host struct */, const uint16_t *dy, int64_t dy_rows,
+                           const int32_t *offsets, const int32_t *perm, int32_t k, int64_t R, uint16_t *dx,
+                           void *stream);
+
+/* SwiGLU a = silu(g) u of h = [g, u] (bf16 [R, 2I], I % 32 == 0), computed in FP32, and
+ * an 8-bit copy of h for the backward: h8 uint8 [R, 2I] E4M3FN bits, h8_scales uint8
+ * [R, 2I/32] E8M0 codes, per 32-block the smallest 2^s with max|h| 2^-s <= 448 (no value
+ * saturates; each is off by at most 2^-4 of itself or 2^-10 2^s).  A block with an
+ * infinity or NaN gets scale code 255 and reads back as NaN.
+ * a: bf16 [R, I] or NULL; aq: MXFP4 [1, R, I] of the bf16 a (as bqm_quantize_mxfp4 gives
+ * it) or NULL.  n_rows: device int32, the rows that hold data (for instance offsets + E;
+ * 4-byte aligned), NULL for all R; the rows behind it are neither read nor written. */
+bqm_status bqm_swiglu_ckpt_fwd(const uint16_t *h, int64_t R, int64_t I, const int32_t *n_rows, uint8_t *h8,
+                               uint8_t *h8_scales, uint16_t *a, bqm_qtensor *aq /* host struct or NULL */,
+                               void *stream);
+
+/* Backward of it from the 8-bit copy, with the routing weight: da bf16 [R, I] is the
+ * gradient of a row's a before its routing weight (bqm_mxfp4_dgrad of the down
+ * projection); with g, u read from h8 and w = topk_w[perm[pos]],
+ *   dg = w da u sig(g) (1 + g (1 - sig(g))),  du = w da silu(g)   -> dh bf16 [R, 2I],
+ *   dtopk_w[perm[pos]] = sum_i da_i silu(g_i) u_i                 -> f32 [R].
+ * perm i32 [R], a permutation of 0 .. R-1 (NULL: pos itself); topk_w f32 [R] (NULL: 1);
+ * dtopk_w may be NULL.  Rows from n_rows on: dh is left as it was, their dtopk_w is 0.
+ * With the checkpoint's g and u in both places, dtopk_w is the derivative that goes with
+ * dh; it differs from <dy, y> by the two roundings of a (8-bit here, MXFP4 there). */
+bqm_status bqm_swiglu_ckpt_bwd(const uint8_t *h8, const uint8_t *h8_scales, const uint16_t *da, const int32_t *perm,
+                               const float *topk_w, int64_t R, int64_t I, const int32_t *n_rows, uint16_t *dh,
+                               float *dtopk_w, void *stream);
+
+/* Balance loss, z-loss and per-expert counts of a routed batch: over the n tokens with
+ * valid[t] != 0 (uint8 [T], NULL: all), p_t = softmax(logits_t), f_e = counts_e / (n k),
+ *   loss[0] = E sum_e f_e mean_t p_te,   loss[1] = mean_t logsumexp(logits_t)^2
+ * (both 0 when n = 0).  counts i32 [E+1]: routed pairs per expert, then n.  Pairs whose
+ * index lies outside [0, E) count for no expert; an index that occurs twice in a token
+ * counts twice.  -inf logits are experts that are switched off; a token with no other
+ * logit has p = 0 and logsumexp 0.  Logits of tokens that do not count may hold anything.
+ * logits f32 [T, E], topk_idx i32 [T, k]; limits as for bqm_route, T * k < 2^31.  Sums of
+ * p are FP32 per workgroup and FP64 across, in a fixed order.  ws:
+ * bqm_router_loss_workspace_size() bytes; calls that share one must not overlap. */
+size_t bqm_router_loss_workspace_size(int64_t T, int32_t E);
+bqm_status bqm_router_loss(const float *logits, const int32_t *topk_idx, const uint8_t *valid, int64_t T, int32_t E,
+                           int32_t k, int32_t *counts, float *loss, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradient of the logits, dlogits f32 [T, E]: of dloss[0] * loss[0] + dloss[1] * loss[1]
+ * (device f32 [2], NULL: no loss) plus sum dtopk_w[t, j] topk_w[t, j] (f32 [T, k], NULL:
+ * none; topk_w as bqm_route gives it with the same renorm), with the indices and counts
+ * held constant.  counts: as bqm_router_loss wrote them for these tokens.  Tokens that do
+ * not count get zeros, and their logits and dtopk_w may hold anything. */
+bqm_status bqm_router_grad(const float *logits, const int32_t *topk_idx, const uint8_t *valid, const int32_t *counts,
+                           const float *dtopk_w, const float *dloss, int64_t T, int32_t E, int32_t k, int32_t renorm,
+                           float *dlogits, void *stream);
 
 /* ---------------------------------------------------------------------------
  * The MoE layer.  Expert weights are stacks w_gu [E, 2I, H] (gate rows 0..I-1,

@@ -1,0 +1,133 @@
+"""Argument checks of the MXFP4 expert and router entry points (host only: every call here
+fails, or is empty, before anything is launched)."""
+import ctypes as C
+
+import pytest
+
+torch = pytest.importorskip("torch")
+bqm = pytest.importorskip("bit_quantized_moe_amd._lib")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return bqm.load()
+
+
+def q(n=1, rows=64, cols=64, fmt=3, codes=16, scales=16):
+    return bqm.QTensorC(fmt, 0, n, rows, cols, codes, scales, None, 1, 0)
+
+
+def test_quantize_mxfp4(lib):
+    f = lib.bqm_quantize_mxfp4
+    assert f(16, C.byref(q(cols=48)), None) == -2 and "multiple of 32" in bqm.bqm_last_error()
+    assert f(16, C.byref(q(fmt=1)), None) == -1
+    assert f(16, C.byref(q(fmt=4)), None) == -1
+    assert f(None, C.byref(q()), None) == -1
+    assert f(24, C.byref(q()), None) == -3
+    assert f(16, C.byref(q(codes=None)), None) == -1
+    assert f(16, C.byref(q(scales=8)), None) == -3
+    assert f(16, C.byref(q(rows=-1)), None) == -1
+    assert f(None, C.byref(q(rows=0)), None) == 0
+    assert f(16, None, None) == -1
+    # the other quantizers and the layer do not take the format
+    assert lib.bqm_quantize_nvfp4(16, 1, None, C.byref(q()), 16, 64, None) == -1
+    assert lib.bqm_quantize_nf4(16, C.byref(q()), None) == -1
+    nested = q()
+    nested.nested = 1
+    assert lib.bqm_dequantize(C.byref(nested), 16, None) == -1
+    d = bqm.MoEDescC(64, 64, 64, 1, 1, 0, 0, 1.0, 0, q(rows=128), q(), None, None, None, None, None)
+    assert lib.bqm_moe_fwd(C.byref(d), 16, 16, 16, 16, 16, 1 << 40, None) == -1
+
+
+def test_gemm(lib):
+    def f(x=None, w=None, off=16, perm=None, k=1, R=64, y=16):
+        return lib.bqm_mxfp4_gemm(C.byref(x or q()), C.byref(w or q(n=4)), off, perm, k, R, y, None)
+    assert f(x=q(fmt=1)) == -1 and f(w=q(n=4, fmt=2)) == -1
+    assert f(x=q(n=2)) == -2                           # x is one matrix
+    assert f(x=q(cols=96)) == -2                       # K differs
+    assert f(x=q(cols=48), w=q(n=4, cols=48)) == -2    # K % 32
+    assert f(w=q(n=4, rows=40)) == -2                  # N % 32
+    assert f(w=q(n=4, rows=0)) == -2 and f(w=q(n=0)) == -2 and f(w=q(n=1025)) == -2
+    assert f(R=63) == -2                               # rows without perm
+    assert f(perm=16, k=2, R=127) == -2 and f(perm=16, k=0, R=64) == -2
+    assert f(R=-1) == -1
+    assert f(off=None) == -1 and f(off=20) == -3 and f(perm=20) == -3
+    assert f(y=None) == -1 and f(y=20) == -3
+    assert f(x=q(codes=None)) == -1 and f(w=q(n=4, scales=18)) == -3
+    assert lib.bqm_mxfp4_gemm(None, C.byref(q()), 16, None, 1, 64, 16, None) == -1
+    assert f(x=q(rows=1 << 30), R=1 << 30) == -2
+    assert f(x=q(rows=0, codes=None, scales=None), R=0, off=None, y=None) == 0
+
+
+def test_dgrad(lib):
+    def f(w=None, dy=16, rows=64, off=16, perm=None, k=1, R=64, dx=16):
+        return lib.bqm_mxfp4_dgrad(C.byref(w or q(n=4)), dy, rows, off, perm, k, R, dx, None)
+    assert f(w=q(fmt=1)) == -1 and f(w=q(rows=33)) == -2 and f(w=q(cols=33)) == -2
+    assert f(rows=63) == -2 and f(perm=16, k=3, R=64) == -2 and f(rows=-1, R=-1) == -1
+    assert f(dy=None) == -1 and f(dx=None) == -1 and f(dy=17) == -3 and f(dx=18) == -3
+    assert f(off=None) == -1
+    assert f(rows=0, R=0, dy=None, dx=None, off=None) == 0
+
+
+def test_swiglu(lib):
+    def f(h=16, R=4, I=64, h8=16, s=16, a=16, aq=None):
+        return lib.bqm_swiglu_ckpt_fwd(h, R, I, None, h8, s, a, None if aq is None else C.byref(aq), None)
+    assert f(I=48) == -2 and f(I=0) == -2 and f(R=-1) == -1 and f(R=1 << 31) == -2
+    assert f(h=None) == -1 and f(h8=None) == -1 and f(s=None) == -1
+    assert f(h=8) == -3 and f(h8=8) == -3 and f(s=8) == -3 and f(a=8) == -3
+    assert f(aq=q(rows=4, fmt=1)) == -1 and f(aq=q(rows=5)) == -2 and f(aq=q(rows=4, codes=None)) == -1
+    assert f(aq=q(rows=4, scales=20)) == -3
+    assert f(R=0, h=None, h8=None, s=None, a=None) == 0
+
+    def g(h8=16, s=16, da=16, perm=16, w=16, R=4, I=64, dh=16, dw=16):
+        return lib.bqm_swiglu_ckpt_bwd(h8, s, da, perm, w, R, I, None, dh, dw, None)
+    assert g(I=16) == -2 and g(R=-2) == -1 and g(da=None) == -1 and g(dh=None) == -1 and g(h8=None) == -1
+    assert g(perm=4) == -3 and g(w=4) == -3 and g(dw=4) == -3 and g(dh=4) == -3
+    assert g(R=0, h8=None, s=None, da=None, dh=None) == 0
+
+
+def test_router(lib):
+    def f(l=16, idx=16, valid=None, T=4, E=8, k=2, counts=16, loss=16, ws=16, wsb=1 << 30):
+        return lib.bqm_router_loss(l, idx, valid, T, E, k, counts, loss, ws, wsb, None)
+    assert f(E=0) == -2 and f(E=1025) == -2 and f(k=9) == -2 and f(k=0) == -2 and f(E=64, k=17) == -2
+    assert f(T=-1) == -1 and f(T=1 << 30) == -2
+    assert f(l=None) == -1 and f(idx=None) == -1 and f(counts=None) == -1 and f(loss=None) == -1
+    assert f(l=8) == -3 and f(valid=8) == -3 and f(loss=8) == -3 and f(ws=8) == -3
+    assert f(ws=None) == -5 and f(wsb=lib.bqm_router_loss_workspace_size(4, 8) - 1) == -5
+    assert lib.bqm_router_loss_workspace_size(-1, 8) == 0 and lib.bqm_router_loss_workspace_size(4, 0) == 0
+    assert lib.bqm_router_loss_workspace_size(1 << 20, 1024) >= lib.bqm_router_loss_workspace_size(1, 1024) > 0
+
+    def g(l=16, idx=16, valid=None, counts=16, dw=None, dl=None, T=4, E=8, k=2, out=16):
+        return lib.bqm_router_grad(l, idx, valid, counts, dw, dl, T, E, k, 0, out, None)
+    assert g(E=2000) == -2 and g(k=9) == -2 and g(T=-1) == -1
+    assert g(l=None) == -1 and g(idx=None) == -1 and g(counts=None) == -1 and g(out=None) == -1
+    assert g(dw=8) == -3 and g(dl=8) == -3 and g(out=8) == -3
+    assert g(T=0, l=None, idx=None, counts=None, out=None) == 0
+
+
+def test_binding_checks_types_shapes_and_layout():
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)  # noqa: E731
+    mxq = lambda n, r, c: bqm.alloc_qtensor(bqm.FMT_MXFP4, n, r, c, device="cpu")  # noqa: E731
+    off, w, x = z(5, dtype=torch.int32), mxq(4, 64, 32), mxq(1, 8, 32)
+    bad = [
+        lambda: bqm.bqm_quantize_mxfp4(z(1, 8, 32, dtype=torch.float32), x),
+        lambda: bqm.bqm_quantize_mxfp4(z(1, 32, 8).transpose(1, 2), x),
+        lambda: bqm.bqm_quantize_mxfp4(z(1, 8, 64), x),
+        lambda: bqm.bqm_mxfp4_gemm(x, w, off[:4], None, 1, z(8, 64)),
+        lambda: bqm.bqm_mxfp4_gemm(x, w, off.long(), None, 1, z(8, 64)),
+        lambda: bqm.bqm_mxfp4_gemm(x, w, off, None, 1, z(8, 32)),
+        lambda: bqm.bqm_mxfp4_gemm(x, w, off, z(7, dtype=torch.int32), 1, z(8, 64)),
+        lambda: bqm.bqm_mxfp4_dgrad(w, z(8, 32), off, None, 1, z(8, 32)),
+        lambda: bqm.bqm_mxfp4_dgrad(w, z(64, 8).t(), off, None, 1, z(8, 32)),
+        lambda: bqm.bqm_swiglu_ckpt_fwd(z(4, 128), z(4, 64, dtype=torch.uint8), z(4, 4, dtype=torch.uint8)),
+        lambda: bqm.bqm_swiglu_ckpt_bwd(z(4, 128, dtype=torch.uint8), z(4, 4, dtype=torch.uint8), z(4, 64),
+                                        z(3, dtype=torch.int32), None, z(4, 128)),
+        lambda: bqm.bqm_router_loss(z(4, 8, dtype=torch.float32), z(4, 2, dtype=torch.int32), z(4, dtype=torch.bool),
+                                    z(9, dtype=torch.int32), z(2, dtype=torch.float32), None),
+        lambda: bqm.bqm_router_grad(z(4, 8), z(4, 2, dtype=torch.int32), None, z(9, dtype=torch.int32), None, None, 0,
+                                    z(4, 8, dtype=torch.float32)),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(bqm.BQMError):
+            f()
+            pytest.fail(f"call {i} went through")
