@@ -17,6 +17,7 @@
 namespace bqm {
 namespace {
 
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(4))) int i32x4;
@@ -50,12 +51,18 @@ struct MxParams {
 __device__ __forceinline__ void dma_b128(const void *g, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(g), "s"(lds) : "memory", "m0");
 }
+// lane i's byte, as a word, lands at lds + 4 i
+__device__ __forceinline__ void dma_u8(const void *g, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, off" : : "v"(g), "s"(lds) : "memory", "m0");
+}
 // workgroup barrier that orders LDS without draining outstanding copies
 __device__ __forceinline__ void barrier_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+  // the builtin, not inline assembly: the compiler then knows which loads have landed
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+  asm volatile("" ::: "memory");  // no read of what the copies wrote before it
 }
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 __device__ __forceinline__ uint32_t lds_addr(const void *p) { return (uint32_t)(uintptr_t)(const lds_void *)p; }
@@ -76,58 +83,55 @@ __device__ __forceinline__ int seg_at(const MxParams &p, int e) {
   return (int)(v < 0 ? 0 : (v > p.R ? p.R : v));
 }
 
-// toff[e] = BM-row tiles of the experts before e, for e = 0 .. E; returns their total
-template <int BM>
-__device__ int tile_prefix(const MxParams &p, int *toff, int *wsum) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  constexpr int PER = kMaxE / NTHR;
-  int c[PER], run = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = tid * PER + i;
-    int n = 0;
-    if (e < p.E) n = seg_at(p, e + 1) - seg_at(p, e);
-    c[i] = n > 0 ? (n + BM - 1) / BM : 0;
-    run += c[i];
-  }
-  int inc = run;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int t = __shfl_up(inc, o, 64);
-    if (lane >= o) inc += t;
-  }
-  if (lane == 63) wsum[wave] = inc;
-  __syncthreads();
-  int base = 0, total = 0;
-#pragma unroll
-  for (int q = 0; q < NTHR / 64; ++q) {
-    if (q < wave) base += wsum[q];
-    total += wsum[q];
-  }
-  int ex = base + inc - run;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = tid * PER + i;
-    if (e <= p.E) toff[e] = ex;
-    ex += c[i];
-  }
-  if (p.E == kMaxE && tid == 0) toff[kMaxE] = total;
-  __syncthreads();
-  return total;
-}
+// Row tiles (of BM rows) in expert order.  Each thread keeps the prefix of its PER experts in
+// registers; the one that owns a row tile's expert tells the others through LDS.
+constexpr int PER = kMaxE / NTHR;
+struct TileMap {
+  int first[PER + 1];  // row tiles before expert PER tid + i
 
-// the expert whose tiles hold row tile mt
-__device__ __forceinline__ int expert_of_tile(const int *toff, int E, int mt) {
-  int lo = 0, hi = E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (toff[mid] <= mt)
-      lo = mid;
-    else
-      hi = mid;
+  // returns the number of row tiles
+  template <int BM>
+  __device__ int build(const MxParams &p, int *wsum) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int c[PER], run = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = tid * PER + i;
+      int n = 0;
+      if (e < p.E) n = seg_at(p, e + 1) - seg_at(p, e);
+      c[i] = n > 0 ? (n + BM - 1) / BM : 0;
+      run += c[i];
+    }
+    int inc = run;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int t = __shfl_up(inc, o, 64);
+      if (lane >= o) inc += t;
+    }
+    if (lane == 63) wsum[wave] = inc;
+    __syncthreads();
+    int base = 0, total = 0;
+#pragma unroll
+    for (int q = 0; q < NTHR / 64; ++q) {
+      if (q < wave) base += wsum[q];
+      total += wsum[q];
+    }
+    first[0] = base + inc - run;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) first[i + 1] = first[i] + c[i];
+    return total;
   }
-  return __builtin_amdgcn_readfirstlane(lo);
-}
+
+  // the owner of row tile mt writes its expert and that expert's first tile to found
+  __device__ __forceinline__ void find(int mt, int *found) const {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (first[i] <= mt && mt < first[i + 1]) {
+        found[0] = (int)threadIdx.x * PER + i;
+        found[1] = first[i];
+      }
+  }
+};
 
 // source row of routed position pos, kept inside the tensor
 __device__ __forceinline__ int64_t src_row(const MxParams &p, int64_t pos) {
@@ -136,315 +140,524 @@ __device__ __forceinline__ int64_t src_row(const MxParams &p, int64_t pos) {
   return r < p.xrows ? r : p.xrows - 1;
 }
 
+// ---------------------------------------------------------------------------
+// the tiled kernels
+// ---------------------------------------------------------------------------
+// A workgroup of four waves (2 x 2) computes BM = 64 TM rows by BN = 64 TN columns of one
+// expert; wave (wm, wn) owns the 32-row tiles 2 tm + wm (interleaved, so that a partly
+// filled tile leaves both row halves the same work) of 32 TN columns.  The contraction goes
+// in steps of 128 bytes per activation row (256 MXFP4 values or 64 bf16 values) through two
+// LDS stages filled by direct-to-LDS copies one step ahead; a step is four slices of
+// VT x TN MFMAs of 32x32.
+//
+// One wave per SIMD (the accumulators of the largest tile take half the register file) has
+// no other wave to hide its waits behind, so the step is written out in issue order: after
+// each MFMA comes a share of the slice's other work (the fragment reads of the next slice,
+// copies of the next step, weight decode), pinned there by scheduling barriers.  The step's
+// one barrier sits inside slice 3, whose fragments are in registers by then: from it on the
+// next step's first fragments are read while slice 3's MFMAs run.
+//
+// 2 x 2 and not 1 x 4 waves: a wave of 128 x 128 reads 8 KB of fragments per 16 MFMAs, one
+// of 256 x 64 10 KB; with the copies into LDS that is 94 against 109 bytes per clock of the
+// LDS's 128 at the MFMA rate.
+//
 // Accumulators hold the product transposed (weights x activations): register v of lane L of
-// tile (tm, tn) is row tm * 32 + L % 32 and column tn * 32 + 8 (v / 4) + 4 (L / 32) + v % 4,
-// so a lane stores 4 consecutive columns of one row at a time.
+// tile (tm, tn) is row L % 32 and column 8 (v / 4) + 4 (L / 32) + v % 4, so a lane stores 4
+// consecutive columns of one row at a time.
+#define MX_PIN() __builtin_amdgcn_sched_barrier(0)
+
+constexpr int DK = 64;   // dgrad: weight rows per step
+constexpr int DQS = 72;  // dgrad: row stride (bf16) of a decoded 64-column group
+
+template <int TM, int TN, bool FWD>
+struct Smem;
 template <int TM, int TN>
-__device__ __forceinline__ void store_tile(const f32x16 (&acc)[TM][TN], uint16_t *out, int64_t ld, int64_t row_base,
-                                           int rows, int col_base, int ncols, int lane) {
-#pragma unroll
-  for (int tm = 0; tm < TM; ++tm) {
-    const int r = tm * 32 + (lane & 31);
-    if (r < rows) {
-      uint16_t *o = out + (row_base + r) * ld;
-#pragma unroll
-      for (int tn = 0; tn < TN; ++tn)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int n = col_base + tn * 32 + 8 * q + 4 * (lane >> 5);
-          if (n < ncols)
-            *reinterpret_cast<uint2 *>(o + n) = make_uint2(pack_bf16_rne(acc[tm][tn][4 * q], acc[tm][tn][4 * q + 1]),
-                                                           pack_bf16_rne(acc[tm][tn][4 * q + 2], acc[tm][tn][4 * q + 3]));
-        }
-    }
-  }
-}
-
+struct Smem<TM, TN, true> {
+  uint8_t a[2][64 * TM * 128];
+  uint8_t b[2][64 * TN * 128];
+  uint32_t s[2][2][2][64 * (TM + TN) + 4];  // [group parity][step of the group][half][row]
+  int wsum[NTHR / 64], found[2];
+};
 template <int TM, int TN>
-__device__ __forceinline__ void clear_acc(f32x16 (&acc)[TM][TN]) {
-#pragma unroll
-  for (int tm = 0; tm < TM; ++tm)
-#pragma unroll
-    for (int tn = 0; tn < TN; ++tn)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[tm][tn][v] = 0.0f;
-}
-
-// ---------------------------------------------------------------------------
-// forward
-// ---------------------------------------------------------------------------
-// A workgroup computes BM = 32 TM rows by 256 columns of one expert; each of its four waves
-// all rows of 64 columns.  K steps of 256 (128 bytes of codes per row, eight MX blocks) go
-// through two LDS stages filled by direct-to-LDS copies one step ahead.  The scales of two
-// steps (16 bytes a row) are loaded to registers and written to LDS regrouped: for each step
-// and half g of a wave, the four scales of a row's blocks g, 2 + g, 4 + g, 6 + g as one word,
-// so that a lane reads one word per operand row and step and the MFMA picks its byte.
-constexpr int BN = 256, BK = 256;
-
-template <int TM>
-struct FwdSmem {
-  uint8_t a[2][32 * TM * 128];
-  uint8_t b[2][BN * 128];
-  uint32_t s[2][2][2][32 * TM + BN];  // [group parity][step of the group][half][row]
-  int toff[kMaxE + 1];
-  int wsum[NTHR / 64];
+struct Smem<TM, TN, false> {
+  uint8_t a[2][64 * TM * 128];
+  uint16_t dq[2][TN][DK * DQS];
+  uint8_t c[2][NTHR / 64][DK * 16 * (TN / 2)];  // each wave's codes of a step: 64 rows of its blocks
+  uint32_t cs[2][NTHR / 64][TN / 2][DK];        // and their scales
+  int wsum[NTHR / 64], found[2];
 };
 
-// the 16 scale bytes of blocks 16 g .. of a row with nb blocks (127 = 2^0 past its end)
+// The scales of blocks 16 g .. 16 g + 15 of a row of nb >= 16 blocks in one load; the last
+// group's 16 bytes end at the row's end, and shift_scales moves them down once they have
+// landed (by the same number of bytes for every row), filling with 127 (2^0).
 __device__ __forceinline__ u32x4 load_scales(const uint8_t *row, int g, int nb) {
-  const uint8_t *p = row + 16 * g;
-  if ((nb & 15) == 0) return *reinterpret_cast<const u32x4 *>(p);
-  u32x4 v = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
-  if ((nb & 3) == 0) {
+  u32x4 v;
+  __builtin_memcpy(&v, row + min(16 * g, nb - 16), 16);  // unaligned where 4 does not divide nb
+  return v;
+}
+__device__ __forceinline__ u32x4 shift_scales(const u32x4 &v, int g, int nb) {
+  const int d = 16 * g - min(16 * g, nb - 16);  // 0 .. 15
+  constexpr uint32_t f = 0x7F7F7F7Fu;
+  // by 8, by 4, then by the remaining 0 to 3 bytes, without a branch
+  const bool by8 = d & 8, by4 = d & 4;
+  auto pick = [](bool c, uint32_t x, uint32_t y) { return c ? x : y; };
+  const uint32_t a0 = pick(by8, v[2], v[0]), a1 = pick(by8, v[3], v[1]), a2 = pick(by8, f, v[2]), a3 = pick(by8, f, v[3]);
+  const uint32_t b0 = pick(by4, a1, a0), b1 = pick(by4, a2, a1), b2 = pick(by4, a3, a2), b3 = pick(by4, f, a3);
+  const uint32_t r = (uint32_t)d & 3u;
+  return u32x4{__builtin_amdgcn_alignbyte(b1, b0, r), __builtin_amdgcn_alignbyte(b2, b1, r),
+               __builtin_amdgcn_alignbyte(b3, b2, r), __builtin_amdgcn_alignbyte(f, b3, r)};
+}
+// the same for a row of fewer than 16 blocks: its bytes at the end of the 16
+__device__ __forceinline__ u32x4 load_few_scales(const uint8_t *row, int nb) {
+  u32x4 v = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (16 * g + 4 * i < nb) v[i] = *reinterpret_cast<const uint32_t *>(p + 4 * i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (16 * g + i < nb) v[i >> 2] = (v[i >> 2] & ~(0xFFu << (8 * (i & 3)))) | ((uint32_t)p[i] << (8 * (i & 3)));
-  }
+  for (int i = 0; i < 16; ++i)
+    if (i >= 16 - nb) v[i >> 2] |= (uint32_t)row[i - (16 - nb)] << (8 * (i & 3));
   return v;
 }
 
-template <int TM>
-__global__ void __launch_bounds__(NTHR, 1) mx_gemm(MxParams p) {
-  constexpr int BM = 32 * TM, TN = 2;
-  constexpr int AR = BM / 32;  // copies of 8 rows per wave: BM / 4 waves / 8
-  __shared__ __attribute__((aligned(16))) FwdSmem<TM> sm;
-  const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
-  const int total = tile_prefix<BM>(p, sm.toff, sm.wsum) * p.NT;
-  // each XCD (workgroups b % 8) walks a contiguous range of tiles, so that the tiles in
-  // flight there share an expert's rows and weights in its L2
-  const int per = (total + 7) / 8;
-  const int first = (blockIdx.x & 7) * per, last = min(first + per, total);
-  const int nb = p.K / 32, nk = (p.K + BK - 1) / BK;
-  for (int L = first + (int)(blockIdx.x >> 3); L < last; L += (int)(gridDim.x >> 3)) {
-    const int mt = L / p.NT, nt = L % p.NT;
-    const int e = expert_of_tile(sm.toff, p.E, mt);
-    const int rb = seg_at(p, e), n_e = seg_at(p, e + 1) - rb;
-    const int m0 = (mt - sm.toff[e]) * BM, n0 = nt * BN;
-    const int rows = min(n_e - m0, BM);
-    const int vt = (rows + 31) / 32;
-    // copy sources at step 0
-    const uint8_t *asrc[AR], *bsrc[8];
-    const int lc = lane & 7;  // position of this lane's chunk in its row
-    const uint8_t *wc = p.wc + (int64_t)e * p.N * (p.K / 2), *ws = p.ws + (int64_t)e * p.N * nb;
-#pragma unroll
-    for (int j = 0; j < AR; ++j) {
-      const int r = 8 * (AR * w + j) + (lane >> 3);
-      asrc[j] = p.xc + src_row(p, (int64_t)rb + min(m0 + r, n_e - 1)) * (p.K / 2);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r = 8 * (8 * w + j) + (lane >> 3);
-      bsrc[j] = wc + (int64_t)min(n0 + r, p.N - 1) * (p.K / 2);
-    }
-    // the rows whose scales this thread carries: weight row tid, and activation row tid
-    const uint8_t *bs = ws + (int64_t)min(n0 + tid, p.N - 1) * nb;
-    const uint8_t *as = tid < BM ? p.xs + src_row(p, (int64_t)rb + min(m0 + tid, n_e - 1)) * nb : nullptr;
-    auto copy = [&](int ks, int st) {
-#pragma unroll
-      for (int j = 0; j < AR; ++j) {
-        const int r = 8 * (AR * w + j) + (lane >> 3), c = 8 * ks + (lc ^ ((r >> 1) & 7));
-        dma_b128(c < nb ? asrc[j] + 16 * c : reinterpret_cast<const uint8_t *>(c_zeros),
-                 lds_addr(sm.a[st]) + 1024 * (AR * w + j));
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = 8 * (8 * w + j) + (lane >> 3), c = 8 * ks + (lc ^ ((r >> 1) & 7));
-        dma_b128(c < nb ? bsrc[j] + 16 * c : reinterpret_cast<const uint8_t *>(c_zeros),
-                 lds_addr(sm.b[st]) + 1024 * (8 * w + j));
-      }
-    };
-    auto put_scales = [&](const u32x4 &v, int buf, int row) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        sm.s[buf][h][0][row] = __builtin_amdgcn_perm(v[2 * h + 1], v[2 * h], 0x06040200u);
-        sm.s[buf][h][1][row] = __builtin_amdgcn_perm(v[2 * h + 1], v[2 * h], 0x07050301u);
-      }
-    };
-    f32x16 acc[TM][TN];
-    clear_acc(acc);
-    __syncthreads();  // the stages of the tile before are free
-    u32x4 sa = {}, sb = load_scales(bs, 0, nb);
-    if (tid < BM) sa = load_scales(as, 0, nb);
-    copy(0, 0);
-    put_scales(sb, 0, BM + tid);
-    if (tid < BM) put_scales(sa, 0, tid);
-    for (int ks = 0; ks < nk; ++ks) {
-      const int st = ks & 1;
-      wait_vm<0>();
-      barrier_lds();
-      const bool odd = ks & 1, more = ks + 1 < nk;
-      if (!odd && ks + 2 < nk) {  // the next group's scales, written at the end of the odd step
-        sb = load_scales(bs, (ks >> 1) + 1, nb);
-        if (tid < BM) sa = load_scales(as, (ks >> 1) + 1, nb);
-      }
-      if (more) copy(ks + 1, st ^ 1);
-      const uint32_t *sw = sm.s[(ks >> 1) & 1][ks & 1][lane >> 5];
-      int ssa[TM], ssb[TN];
-#pragma unroll
-      for (int tm = 0; tm < TM; ++tm) ssa[tm] = (int)sw[tm * 32 + (lane & 31)];
-#pragma unroll
-      for (int tn = 0; tn < TN; ++tn) ssb[tn] = (int)sw[BM + 64 * w + tn * 32 + (lane & 31)];
-      auto slice = [&](auto KK) {
-        constexpr int kk = KK.value;
-        const int c = 2 * kk + (lane >> 5);
-        i32x4 bf[TN];
-#pragma unroll
-        for (int tn = 0; tn < TN; ++tn)
-          bf[tn] = *reinterpret_cast<const i32x4 *>(sm.b[st] + swz(64 * w + tn * 32 + (lane & 31), c));
-#pragma unroll
-        for (int tm = 0; tm < TM; ++tm) {
-          const i32x4 af = *reinterpret_cast<const i32x4 *>(sm.a[st] + swz(tm * 32 + (lane & 31), c));
-          const i32x8 a8 = {af[0], af[1], af[2], af[3], 0, 0, 0, 0};
-          if (tm < vt) {
-#pragma unroll
-            for (int tn = 0; tn < TN; ++tn) {
-              const i32x8 b8 = {bf[tn][0], bf[tn][1], bf[tn][2], bf[tn][3], 0, 0, 0, 0};
-              acc[tm][tn] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, acc[tm][tn], 4, 4, kk, ssb[tn], kk,
-                                                                            ssa[tm]);
-            }
-          }
-        }
-      };
-      slice(std::integral_constant<int, 0>{});
-      slice(std::integral_constant<int, 1>{});
-      slice(std::integral_constant<int, 2>{});
-      slice(std::integral_constant<int, 3>{});
-      if (odd && more) {
-        put_scales(sb, ((ks >> 1) + 1) & 1, BM + tid);
-        if (tid < BM) put_scales(sa, ((ks >> 1) + 1) & 1, tid);
-      }
-    }
-    store_tile<TM, TN>(acc, p.out, p.N, (int64_t)rb + m0, rows, n0 + 64 * w, p.N, lane);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// dgrad
-// ---------------------------------------------------------------------------
-// A workgroup computes BM rows by 256 columns (of k) of one expert, in steps of 64 weight
-// rows n.  dY goes to LDS by direct copies one step ahead.  Each wave owns 64 columns, that
-// is two MX blocks of every weight row: lane i of the wave loads row i's two blocks (32 bytes
-// and two scales), decodes them to bf16 and writes them to the wave's own 64 x 64 LDS tile,
-// from which the 16-bit transposing read hands every lane one column's 8 consecutive rows.
-constexpr int DK = 64;   // weight rows per step
-constexpr int DQS = 72;  // row stride (bf16) of the decoded tile
-
-template <int TM>
-struct DgradSmem {
-  uint8_t a[2][32 * TM * 128];        // bf16 dY, 64 of n per row
-  uint16_t dq[NTHR / 64][DK * DQS];
-  int toff[kMaxE + 1];
-  int wsum[NTHR / 64];
-};
-
-// B fragment (8 consecutive rows of one column per lane) of the decoded tile
-__device__ __forceinline__ bf16x8 frag_trans(const uint16_t *t, int kbase, int nbase, int lane) {
+// B fragment (8 consecutive rows of one column per lane) of a decoded 64-column group
+__device__ __forceinline__ i32x4 frag_trans(const uint16_t *t, int kbase, int nbase, int lane) {
   const int g = lane >> 4, s = lane & 15;
   const uint16_t *p = t + (kbase + 8 * (g >> 1) + (s >> 2)) * DQS + nbase + 16 * (g & 1) + 4 * (s & 3);
   const s16x4 h0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p));
   const s16x4 h1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * DQS));
   const s16x8 v = {h0[0], h0[1], h0[2], h0[3], h1[0], h1[1], h1[2], h1[3]};
-  return __builtin_bit_cast(bf16x8, v);
+  return __builtin_bit_cast(i32x4, v);
 }
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 template <int P>
 __device__ __forceinline__ uint32_t fp4_bf16(uint32_t c, float sc) {
   return __builtin_bit_cast(uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, P));
 }
 
-// one MX block (32 codes) -> 32 bf16 at dst; sc: its E8M0 code
-__device__ __forceinline__ void decode_block(const u32x4 &c, uint32_t sc, uint16_t *dst) {
-  const float s = sc == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(sc ? sc << 23 : 0x00400000u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const u32x4 o = {fp4_bf16<0>(c[i], s), fp4_bf16<1>(c[i], s), fp4_bf16<2>(c[i], s), fp4_bf16<3>(c[i], s)};
-    *reinterpret_cast<u32x4 *>(dst + 8 * i) = o;
-  }
+__device__ __forceinline__ float e8m0(uint32_t c) {
+  return c == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(c ? c << 23 : 0x00400000u);
 }
 
-template <int TM>
-__global__ void __launch_bounds__(NTHR, 1) mx_dgrad(MxParams p) {
-  constexpr int BM = 32 * TM, TN = 2, AR = BM / 32;
-  __shared__ __attribute__((aligned(16))) DgradSmem<TM> sm;
-  const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
-  const int total = tile_prefix<BM>(p, sm.toff, sm.wsum) * p.NT;
-  const int per = (total + 7) / 8;
-  const int first = (blockIdx.x & 7) * per, last = min(first + per, total);
-  const int nb = p.K / 32, nk = (p.N + DK - 1) / DK;
-  for (int L = first + (int)(blockIdx.x >> 3); L < last; L += (int)(gridDim.x >> 3)) {
-    const int mt = L / p.NT, nt = L % p.NT;
-    const int e = expert_of_tile(sm.toff, p.E, mt);
-    const int rb = seg_at(p, e), n_e = seg_at(p, e + 1) - rb;
-    const int m0 = (mt - sm.toff[e]) * BM;
-    const int rows = min(n_e - m0, BM);
-    const int vt = (rows + 31) / 32;
-    const uint16_t *asrc[AR];
+// Everything a wave keeps while it works on one tile.
+template <int TM, int TN, bool FWD>
+struct Tile {
+  static constexpr int BM = 64 * TM, BN = 64 * TN;
+  static constexpr int DB = TN / 2;  // dgrad: MX blocks a lane decodes per step
+  static constexpr int kCodeOps = 2 * DB;  // dgrad: copies of codes and of scales per step
+  const MxParams &p;
+  Smem<TM, TN, FWD> &sm;
+  int lane, w, wm, wn, nb, nk;
+  const uint8_t *asrc[2 * TM];  // activation rows of this lane's copies (bytes)
+  int alen;                     // bytes of an activation row
+  const uint8_t *zeros;
+  const uint8_t *wbase;         // the expert's codes
+  uint32_t boff[FWD ? 2 * TN : 1];
+  const uint8_t *sa, *sb;       // forward: the scale rows this thread carries
+  u32x4 va, vb;                 // their 16 bytes of the next group
+  u32x4 cc[DB];                 // dgrad: codes of the next step
+  uint32_t sc[DB];              // and their scales
+  int q0;                       // dgrad: first block of this wave
+  i32x4 af[2][TM], bf[2][TN];
+  int ssa[TM], ssb[TN];         // forward: scale words of the step
+  f32x16 acc[TM][TN];
+
+  __device__ __forceinline__ Tile(const MxParams &p_, Smem<TM, TN, FWD> &sm_) : p(p_), sm(sm_) {
+    lane = threadIdx.x & 63;
+    w = wave_id();
+    wm = w >> 1;
+    wn = w & 1;
+    nb = p.K / 32;
+    nk = FWD ? (p.K + 255) / 256 : (p.N + DK - 1) / DK;
+    alen = FWD ? p.K / 2 : p.N * 2;
+    zeros = reinterpret_cast<const uint8_t *>(c_zeros);
+  }
+
+  // rb: the expert's first row, m0: the tile's, within n_e rows; n0: the tile's first column
+  __device__ __forceinline__ void setup(int e, int rb, int m0, int n_e, int n0) {
+    const int tid = threadIdx.x;
+    // what follows from the lane is computed anew for each tile: kept across tiles it is
+    // spilled, and the wait for its reload lands inside the K loop
+    asm volatile("" : "+v"(lane));
 #pragma unroll
-    for (int j = 0; j < AR; ++j) {
-      const int r = 8 * (AR * w + j) + (lane >> 3);
-      asrc[j] = p.dy + src_row(p, (int64_t)rb + min(m0 + r, n_e - 1)) * p.N;
+    for (int j = 0; j < 2 * TM; ++j) {
+      const int r = 8 * (2 * TM * w + j) + (lane >> 3);
+      const int64_t row = src_row(p, (int64_t)rb + min(m0 + r, n_e - 1));
+      asrc[j] = (FWD ? p.xc : reinterpret_cast<const uint8_t *>(p.dy)) + row * alen;
     }
-    // the two MX blocks of this wave's 64 columns (past the row's end: its last block,
-    // whose columns are dropped)
-    const int b0 = min((nt * 256 + 64 * w) / 32, nb - 1), b1 = min(b0 + 1, nb - 1);
-    const uint8_t *wc = p.wc + (int64_t)e * p.N * (p.K / 2), *ws = p.ws + (int64_t)e * p.N * nb;
-    auto copy = [&](int ks, int st) {
+    wbase = p.wc + (int64_t)e * p.N * (p.K / 2);
+    const uint8_t *ws = p.ws + (int64_t)e * p.N * nb;
+    if constexpr (FWD) {
 #pragma unroll
-      for (int j = 0; j < AR; ++j) {
-        const int r = 8 * (AR * w + j) + (lane >> 3), n = DK * ks + 8 * ((lane & 7) ^ ((r >> 1) & 7));
-        dma_b128(n < p.N ? reinterpret_cast<const void *>(asrc[j] + n) : reinterpret_cast<const void *>(c_zeros),
-                 lds_addr(sm.a[st]) + 1024 * (AR * w + j));
-      }
-    };
-    u32x4 wc0, wc1;
-    uint32_t ws0, ws1;
-    auto load_w = [&](int ks) {  // rows past N: the last row's (their dY is zero)
+      for (int j = 0; j < 2 * TN; ++j) boff[j] = (uint32_t)min(n0 + 8 * (2 * TN * w + j) + (lane >> 3), p.N - 1) * (p.K / 2);
+      sb = ws + (int64_t)min(n0 + (tid < BN ? tid : 0), p.N - 1) * nb;
+      sa = p.xs + src_row(p, (int64_t)rb + min(m0 + (tid < BM ? tid : 0), n_e - 1)) * nb;
+    } else {
+      sb = ws;
+      q0 = n0 / 32 + w * DB;
+    }
+  }
+
+  // copy j of step ks into stage st: activations (j < 2 TM; zeros past the row's end), then
+  // weights (any of the row's bytes there)
+  __device__ __forceinline__ void copy(int j, int ks, int st) {
+    if (j < 2 * TM) {
+      const int r = 8 * (2 * TM * w + j) + (lane >> 3);
+      const int o = 128 * ks + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+      dma_b128(o < alen ? asrc[j] + o : zeros,
+               lds_addr(sm.a[st]) + 1024 * (2 * TM * w + j));
+    } else if constexpr (FWD) {
+      j -= 2 * TM;
+      const int r = 8 * (2 * TN * w + j) + (lane >> 3);
+      const int o = 128 * ks + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+      dma_b128(wbase + (boff[j] + (uint32_t)(o < alen ? o : 0)), lds_addr(sm.b[st]) + 1024 * (2 * TN * w + j));
+    }
+  }
+
+  // ---- forward: scales of a group of two steps, loaded by the thread of their row (threads
+  // past the tile's rows load row 0's and drop them) ----
+  __device__ __forceinline__ void get_scales(int group) {
+    va = load_scales(sa, group, nb);
+    vb = load_scales(sb, group, nb);
+  }
+  // for each step and half g of a wave: the scales of blocks g, 2 + g, 4 + g, 6 + g as one
+  // word, of which the MFMA of slice kk takes byte kk
+  __device__ __forceinline__ void put_words(const u32x4 &v, int group, int row) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t(&s)[2][64 * (TM + TN) + 4] = sm.s[group & 1][h];
+      s[0][row] = __builtin_amdgcn_perm(v[2 * h + 1], v[2 * h], 0x06040200u);
+      s[1][row] = __builtin_amdgcn_perm(v[2 * h + 1], v[2 * h], 0x07050301u);
+    }
+  }
+  __device__ __forceinline__ void put_scales(int group) {
+    // threads without a row write to a word past the rows': a branch here would let the
+    // compiler move MFMAs past it, out of their order
+    const int tid = threadIdx.x, none = BM + BN;
+    put_words(shift_scales(va, group, nb), group, BM == NTHR || tid < BM ? tid : none);
+    put_words(shift_scales(vb, group, nb), group, BN == NTHR || tid < BN ? BM + tid : none);
+  }
+  __device__ __forceinline__ const uint32_t *scale_words(int ks) const { return sm.s[(ks >> 1) & 1][ks & 1][lane >> 5]; }
+
+  // ---- dgrad: lane i of a wave decodes DB blocks of weight row i of the step ----
+  // The codes go to the wave's own LDS area two steps ahead (copies and not loads to
+  // registers: the compiler would wait for those without counting the copies in between).
+  // Row r keeps its half h of 32 bytes at h ^ (r >> 3 & 1) against bank conflicts.
+  __device__ __forceinline__ void code_op(int i, int ks) {
+    const int d = ks & 1;
+    if (i < DB) {
+      const int r = (64 / DB) * i + lane / DB, h = DB == 2 ? (lane & 1) ^ ((r >> 3) & 1) : 0;
+      const int64_t n = min(DK * ks + r, p.N - 1);  // past the end: the last row (its dY is zero)
+      const int q = min(q0 + h, nb - 1);            // past the end: columns that are dropped
+      dma_b128(wbase + n * (p.K / 2) + 16 * q, lds_addr(sm.c[d][w]) + 1024 * i);
+    } else {
       const int64_t n = min(DK * ks + lane, p.N - 1);
-      wc0 = *reinterpret_cast<const u32x4 *>(wc + n * (p.K / 2) + 16 * b0);
-      wc1 = *reinterpret_cast<const u32x4 *>(wc + n * (p.K / 2) + 16 * b1);
-      ws0 = ws[n * nb + b0];
-      ws1 = ws[n * nb + b1];
-    };
-    f32x16 acc[TM][TN];
-    clear_acc(acc);
-    __syncthreads();  // the stages of the tile before are free
-    uint16_t *dq = sm.dq[w];
-    load_w(0);
-    copy(0, 0);
-    for (int ks = 0; ks < nk; ++ks) {
-      const int st = ks & 1;
-      wait_vm<0>();
-      barrier_lds();
-      decode_block(wc0, ws0, dq + lane * DQS);
-      decode_block(wc1, ws1, dq + lane * DQS + 32);
-      if (ks + 1 < nk) {
-        load_w(ks + 1);
-        copy(ks + 1, st ^ 1);
-      }
+      dma_u8(sb + n * nb + min(q0 + i - DB, nb - 1), lds_addr(sm.cs[d][w][i - DB]));
+    }
+  }
+  __device__ __forceinline__ void read_codes(int ks) {
+    const int d = ks & 1;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        bf16x8 bf[TN];
-#pragma unroll
-        for (int tn = 0; tn < TN; ++tn) bf[tn] = frag_trans(dq, 16 * kk, 32 * tn, lane);
-#pragma unroll
-        for (int tm = 0; tm < TM; ++tm) {
-          const bf16x8 af = *reinterpret_cast<const bf16x8 *>(sm.a[st] + swz(tm * 32 + (lane & 31), 2 * kk + (lane >> 5)));
-          if (tm < vt) {
-#pragma unroll
-            for (int tn = 0; tn < TN; ++tn)
-              acc[tm][tn] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[tn], af, acc[tm][tn], 0, 0, 0);
+    for (int b = 0; b < DB; ++b) {
+      const int h = DB == 2 ? b ^ ((lane >> 3) & 1) : 0;
+      cc[b] = *reinterpret_cast<const u32x4 *>(sm.c[d][w] + 16 * (DB * lane + h));
+      sc[b] = sm.cs[d][w][b][lane];
+    }
+  }
+  // quarter u of the lane's blocks -> bf16 (exact) in buffer d
+  __device__ __forceinline__ void decode(int u, int d) {
+    const int b = u >> 2, i = u & 3, blk = w * DB + b;
+    const float f = e8m0(sc[b]);
+    const u32x4 o = {fp4_bf16<0>(cc[b][i], f), fp4_bf16<1>(cc[b][i], f), fp4_bf16<2>(cc[b][i], f),
+                     fp4_bf16<3>(cc[b][i], f)};
+    *reinterpret_cast<u32x4 *>(sm.dq[d][blk >> 1] + lane * DQS + 32 * (blk & 1) + 8 * i) = o;
+  }
+
+  // ---- fragments of slice kk of stage st into set k ----
+  __device__ __forceinline__ void read_a(int k, int tm, int kk, int st) {
+    af[k][tm] = *reinterpret_cast<const i32x4 *>(sm.a[st] + swz(32 * (2 * tm + wm) + (lane & 31), 2 * kk + (lane >> 5)));
+  }
+  __device__ __forceinline__ void read_b(int k, int tn, int kk, int st) {
+    const int c = 32 * (wn * TN + tn);
+    if constexpr (FWD)
+      bf[k][tn] = *reinterpret_cast<const i32x4 *>(sm.b[st] + swz(c + (lane & 31), 2 * kk + (lane >> 5)));
+    else
+      bf[k][tn] = frag_trans(sm.dq[st][c >> 6], 16 * kk, c & 63, lane);
+  }
+
+  template <int KK>
+  __device__ __forceinline__ void mfma(int k, int tm, int tn) {
+    const i32x4 a = af[k][tm], b = bf[k][tn];
+    if constexpr (FWD) {
+      const i32x8 a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+      acc[tm][tn] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, acc[tm][tn], 4, 4, KK, ssb[tn], KK, ssa[tm]);
+    } else {
+      acc[tm][tn] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a),
+                                                            acc[tm][tn], 0, 0, 0);
+    }
+  }
+
+  // The copies of step ks + 2 go into the stage that step ks has finished reading: the first
+  // half from slice 3 of step ks on (after its barrier), the rest in slice 0 of step ks + 1.
+  // LEFT: steps that follow (0, 1, or 2 for more).  PAR: the step's parity (-1: not known).
+  static constexpr int kCopies = 2 * TM + (FWD ? 2 * TN : 0), kFirst = kCopies / 2;
+
+  // Copies of this wave that its wait in slice 3 may leave in flight: those for later steps
+  // than the next
+  template <int LEFT>
+  static constexpr int in_flight() {
+    return !FWD && LEFT > 1 ? kCodeOps : 0;
+  }
+
+  // other work of slices 0-2, item i: fragment reads of the next slice, then copies and what
+  // becomes of them.  Slice 0: the rest of the next step's copies; forward: the scales of
+  // the next group (even steps); dgrad: the codes of the step after the next.  Slice 1:
+  // dgrad: the next step's codes are read and half decoded.  Slice 2: scales written, or the
+  // rest decoded.
+  template <int VT, int KK, int LEFT, int PAR>
+  static constexpr int items() {
+    const int reads = TN + VT;
+    if (LEFT == 0) return reads;
+    if (KK == 0) return reads + (kCopies - kFirst) + (FWD ? (PAR == 0 ? 1 : 0) : in_flight<LEFT>());
+    if (KK == 1) return reads + (FWD ? 0 : 1 + 2 * DB);
+    return reads + (FWD ? 1 : 2 * DB);
+  }
+  template <int VT, int KK, int LEFT, int PAR>
+  __device__ __forceinline__ void item(int i, int ks, int st) {
+    constexpr int k = (KK + 1) & 1;
+    if (i < TN) return read_b(k, i, KK + 1, st);
+    i -= TN;
+    if (i < VT) return read_a(k, i, KK + 1, st);
+    i -= VT;
+    if constexpr (LEFT > 0) {
+      if constexpr (KK == 0) {
+        if (i < kCopies - kFirst) return copy(kFirst + i, ks + 1, st ^ 1);
+        i -= kCopies - kFirst;
+        if constexpr (FWD) {
+          // the next group, or the last again (it is then not used)
+          get_scales(min((ks >> 1) + 1, (nb - 1) >> 4));
+        } else {
+          code_op(i, ks + 2);
+        }
+      } else if constexpr (KK == 1) {
+        if constexpr (!FWD) {
+          if (i == 0) {
+            // this wave's codes of the next step, older than the copies of the step after
+            // it (the first kFirst) and than what slice 0 issued
+            if constexpr (LEFT > 1)
+              wait_vm<kCopies + kCodeOps>();
+            else
+              wait_vm<kCopies - kFirst>();
+            read_codes(ks + 1);
+          } else {
+            decode(i - 1, st ^ 1);
           }
+        }
+      } else {
+        if constexpr (FWD) {
+          if constexpr (PAR != 0) put_scales((ks >> 1) + 1);  // (at an even step of no known parity: not read)
+        } else {
+          decode(2 * DB + i, st ^ 1);
         }
       }
     }
-    store_tile<TM, TN>(acc, p.out, p.K, (int64_t)rb + m0, rows, nt * 256 + 64 * w, p.K, lane);
+  }
+
+  template <int VT, int KK, int LEFT, int PAR>
+  __device__ __forceinline__ void slice(int ks, int st) {
+    constexpr int NP = VT * TN, NI = items<VT, KK, LEFT, PAR>();
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+      mfma<KK>(KK & 1, q / TN, q % TN);
+#pragma unroll
+      for (int i = q * NI / NP; i < (q + 1) * NI / NP; ++i) item<VT, KK, LEFT, PAR>(i, ks, st);
+      MX_PIN();
+    }
+  }
+
+  // slice 3: its first MFMA, then the step's barrier, then slice 0 of the next step is read
+  // and the copies of the step after it begin
+  template <int VT, int LEFT>
+  __device__ __forceinline__ void slice3(int ks, int st) {
+    constexpr int NP = VT * TN, NR = TN + VT, NW = FWD ? NR : 0, NI = NR + NW + (LEFT > 1 ? kFirst : 0);
+    int na[TM], nw[TN];
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+      mfma<3>(1, q / TN, q % TN);
+      if constexpr (LEFT > 0) {
+        if (q == 0) {
+          // every wave is done reading stage st, and the next stage is whole
+          MX_PIN();
+          wait_vm<in_flight<LEFT>()>();
+          barrier_lds();
+          MX_PIN();
+        }
+        const uint32_t *sw = nullptr;
+        if constexpr (FWD) sw = scale_words(ks + 1);
+#pragma unroll
+        for (int i = q * NI / NP; i < (q + 1) * NI / NP; ++i) {
+          if (i < TN)
+            read_b(0, i, 0, st ^ 1);
+          else if (i < NR)
+            read_a(0, i - TN, 0, st ^ 1);
+          else if (i < NR + NW) {
+            const int j = i - NR;
+            if (j < TN)
+              nw[j] = (int)sw[BM + 32 * (wn * TN + j) + (lane & 31)];
+            else
+              na[j - TN] = (int)sw[32 * (2 * (j - TN) + wm) + (lane & 31)];
+          } else {
+            copy(i - NR - NW, ks + 2, st);
+          }
+        }
+      }
+      MX_PIN();
+    }
+    if constexpr (FWD && LEFT > 0) {
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn) ssb[tn] = nw[tn];
+#pragma unroll
+      for (int tm = 0; tm < VT; ++tm) ssa[tm] = na[tm];
+    }
+  }
+
+  template <int VT, int LEFT, int PAR>
+  __device__ __forceinline__ void step(int ks, int st) {
+    slice<VT, 0, LEFT, PAR>(ks, st);
+    slice<VT, 1, LEFT, PAR>(ks, st);
+    slice<VT, 2, LEFT, PAR>(ks, st);
+    slice3<VT, LEFT>(ks, st);
+  }
+
+  // the contraction of one tile of which VT row tiles per wave hold rows
+  template <int VT>
+  __device__ __forceinline__ void run() {
+#pragma unroll
+    for (int tm = 0; tm < VT; ++tm)
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[tm][tn][v] = 0.0f;
+    if constexpr (FWD) {
+      if (nb >= 16) {
+        get_scales(0);
+      } else {  // in the place where the others' loads end
+        va = load_few_scales(sa, nb);
+        vb = load_few_scales(sb, nb);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCodeOps; ++i) code_op(i, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < kCopies; ++j) copy(j, 0, 0);
+    if constexpr (FWD) {
+      put_scales(0);
+    } else {
+      wait_vm<kCopies>();  // this wave's codes
+      read_codes(0);
+#pragma unroll
+      for (int u = 0; u < 4 * DB; ++u) decode(u, 0);
+#pragma unroll
+      for (int i = 0; i < kCodeOps; ++i) code_op(i, 1);
+    }
+    wait_vm<0>();
+    barrier_lds();
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn) read_b(0, tn, 0, 0);
+#pragma unroll
+    for (int tm = 0; tm < VT; ++tm) read_a(0, tm, 0, 0);
+    if constexpr (FWD) {
+      const uint32_t *sw = scale_words(0);
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn) ssb[tn] = (int)sw[BM + 32 * (wn * TN + tn) + (lane & 31)];
+#pragma unroll
+      for (int tm = 0; tm < VT; ++tm) ssa[tm] = (int)sw[32 * (2 * tm + wm) + (lane & 31)];
+    }
+    if (nk > 1) {
+#pragma unroll
+      for (int j = 0; j < kFirst; ++j) copy(j, 1, 1);
+    }
+    int ks = 0;
+    for (; ks + 3 < nk; ks += 2) {
+      step<VT, 2, 0>(ks, 0);
+      step<VT, 2, 1>(ks + 1, 1);
+    }
+    if (ks + 3 == nk) step<VT, 2, 0>(ks++, 0);
+    if (ks + 2 == nk) {
+      step<VT, 1, -1>(ks, ks & 1);
+      ++ks;
+    }
+    step<VT, 0, -1>(ks, ks & 1);
+  }
+
+  // rows: those of the tile that exist; ncols: columns of the output
+  template <int VT>
+  __device__ __forceinline__ void store(int64_t row_base, int rows, int n0, int ncols) {
+#pragma unroll
+    for (int tm = 0; tm < VT; ++tm) {
+      const int r = 32 * (2 * tm + wm) + (lane & 31);
+      if (r < rows) {
+        uint16_t *o = p.out + (row_base + r) * ncols;
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int n = n0 + 32 * (wn * TN + tn) + 8 * q + 4 * (lane >> 5);
+            if (n < ncols)
+              *reinterpret_cast<uint2 *>(o + n) = make_uint2(pack_bf16_rne(acc[tm][tn][4 * q], acc[tm][tn][4 * q + 1]),
+                                                             pack_bf16_rne(acc[tm][tn][4 * q + 2], acc[tm][tn][4 * q + 3]));
+          }
+      }
+    }
+  }
+
+  template <int VT>
+  __device__ __forceinline__ void run_and_store(int64_t row_base, int rows, int n0, int ncols) {
+    run<VT>();
+    store<VT>(row_base, rows, n0, ncols);
+  }
+};
+
+template <int TM, int TN, bool FWD, int OCC>
+__global__ void __launch_bounds__(NTHR, OCC) mx_tiles(MxParams p) {
+  __shared__ __attribute__((aligned(16))) Smem<TM, TN, FWD> sm;
+  constexpr int BM = 64 * TM, BN = 64 * TN;
+  const int ncols = FWD ? p.N : p.K;
+  TileMap map;
+  const int total = map.build<BM>(p, sm.wsum) * p.NT;
+  // each XCD (workgroups b % 8) walks a contiguous range of tiles, so that the tiles in
+  // flight there share an expert's rows and weights in its L2
+  const int per = (total + 7) / 8;
+  const int first = (blockIdx.x & 7) * per, last = min(first + per, total);
+  Tile<TM, TN, FWD> t(p, sm);
+  for (int L = first + (int)(blockIdx.x >> 3); L < last; L += (int)(gridDim.x >> 3)) {
+    const int mt = L / p.NT, n0 = (L % p.NT) * BN;
+    map.find(mt, sm.found);
+    barrier_lds();  // also: the stages of the tile before are free
+    const int e = __builtin_amdgcn_readfirstlane(sm.found[0]);
+    const int rb = seg_at(p, e), n_e = seg_at(p, e + 1) - rb;
+    const int m0 = (mt - __builtin_amdgcn_readfirstlane(sm.found[1])) * BM;
+    const int rows = min(n_e - m0, BM);
+    const int vt = (rows + 63) / 64;  // row tiles per wave that hold rows
+    t.setup(e, rb, m0, n_e, n0);
+    const int64_t row_base = (int64_t)rb + m0;
+    if constexpr (TM == 1) {
+      t.template run_and_store<1>(row_base, rows, n0, ncols);
+    } else if constexpr (TM == 2) {
+      if (vt == 2)
+        t.template run_and_store<2>(row_base, rows, n0, ncols);
+      else
+        t.template run_and_store<1>(row_base, rows, n0, ncols);
+    } else {
+      if (vt == 4)
+        t.template run_and_store<4>(row_base, rows, n0, ncols);
+      else if (vt == 3)
+        t.template run_and_store<3>(row_base, rows, n0, ncols);
+      else if (vt == 2)
+        t.template run_and_store<2>(row_base, rows, n0, ncols);
+      else
+        t.template run_and_store<1>(row_base, rows, n0, ncols);
+    }
   }
 }
+#undef MX_PIN
 
 // ---------------------------------------------------------------------------
 // host side
@@ -484,6 +697,7 @@ bqm_status check_routed(const char *who, const bqm_qtensor *w, const int32_t *of
   } else {
     BQM_REQUIRE(rows == R, BQM_ERR_SHAPE, "%s: R=%lld, but %lld rows and no perm", who, (long long)R, (long long)rows);
   }
+  BQM_REQUIRE(w->rows * (w->cols / 2) < ((int64_t)1 << 32), BQM_ERR_SHAPE, "%s: one expert's codes reach 4 GiB", who);
   BQM_REQUIRE((R / 32 + w->n_mat) * cdiv(w->rows > w->cols ? w->rows : w->cols, 32) < ((int64_t)1 << 31),
               BQM_ERR_SHAPE, "%s: too many tiles", who);
   if (R == 0) return BQM_OK;
@@ -496,11 +710,26 @@ bqm_status check_routed(const char *who, const bqm_qtensor *w, const int32_t *of
 
 constexpr int kCUs = 256;
 
-// workgroups for at most R / bm + E row tiles of nt column tiles, one resident per CU
-unsigned tile_grid(int64_t R, int E, int bm, int64_t nt) {
-  const int64_t tiles = (R / bm + (E < R ? E : R)) * nt;
-  const int64_t g = cdiv(tiles < kCUs ? tiles : kCUs, 8) * 8;
-  return (unsigned)g;
+// Tile size by the rows an expert has on average (the host knows R and E, not the offsets).
+constexpr int64_t kBigRows = 96;
+
+template <bool FWD>
+bqm_status launch_tiles(MxParams p, hipStream_t s, const char *what) {
+  const int64_t ncols = FWD ? p.N : p.K;
+  auto go = [&](auto TM, auto TN, auto OCC) {
+    constexpr int BM = 64 * TM.value, BN = 64 * TN.value;
+    p.NT = (int)cdiv(ncols, BN);
+    // at most R / BM + E row tiles; as many workgroups as the chip holds at once
+    const int64_t tiles = (p.R / BM + (p.E < p.R ? p.E : p.R)) * p.NT, slots = (int64_t)kCUs * OCC.value;
+    const unsigned grid = (unsigned)(cdiv(tiles < slots ? tiles : slots, 8) * 8);
+    mx_tiles<TM.value, TN.value, FWD, OCC.value><<<grid, NTHR, 0, s>>>(p);
+  };
+  using std::integral_constant;
+  if (p.R >= kBigRows * p.E)
+    go(integral_constant<int, 4>{}, integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  else
+    go(integral_constant<int, 1>{}, integral_constant<int, 2>{}, integral_constant<int, 2>{});
+  return launch_status(what);
 }
 
 }  // namespace
@@ -535,11 +764,9 @@ extern "C" bqm_status bqm_mxfp4_gemm(const bqm_qtensor *x, const bqm_qtensor *w,
   p.k = k;
   p.N = (int)w->rows;
   p.K = (int)w->cols;
-  p.NT = (int)cdiv(p.N, BN);
   p.R = R;
   p.out = y;
-  mx_gemm<8><<<tile_grid(R, p.E, 256, p.NT), NTHR, 0, as_stream(stream)>>>(p);
-  return launch_status("mx_gemm");
+  return launch_tiles<true>(p, as_stream(stream), who);
 }
 
 extern "C" bqm_status bqm_mxfp4_dgrad(const bqm_qtensor *w, const uint16_t *dy, int64_t dy_rows,
@@ -562,9 +789,7 @@ extern "C" bqm_status bqm_mxfp4_dgrad(const bqm_qtensor *w, const uint16_t *dy, 
   p.k = k;
   p.N = (int)w->rows;
   p.K = (int)w->cols;
-  p.NT = (int)cdiv(p.K, 256);
   p.R = R;
   p.out = dx;
-  mx_dgrad<8><<<tile_grid(R, p.E, 256, p.NT), NTHR, 0, as_stream(stream)>>>(p);
-  return launch_status("mx_dgrad");
+  return launch_tiles<false>(p, as_stream(stream), who);
 }
