@@ -51,9 +51,22 @@ struct MxParams {
 __device__ __forceinline__ void dma_b128(const void *g, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(g), "s"(lds) : "memory", "m0");
 }
+// The same with a scalar base and a lane's byte offset: no vector instruction per copy.
+__device__ __forceinline__ void dma_b128(const void *base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(lds)
+               : "memory", "m0");
+}
 // lane i's byte, as a word, lands at lds + 4 i
 __device__ __forceinline__ void dma_u8(const void *g, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, off" : : "v"(g), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void dma_u8(const void *base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(lds)
+               : "memory", "m0");
 }
 // workgroup barrier that orders LDS without draining outstanding copies
 __device__ __forceinline__ void barrier_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
@@ -236,7 +249,12 @@ __device__ __forceinline__ float e8m0(uint32_t c) {
 }
 
 // Everything a wave keeps while it works on one tile.
-template <int TM, int TN, bool FWD>
+// FAST: the contraction is whole steps and every source lies within 4 GiB of a base, so a
+// copy's address is a scalar base that moves with the step plus the lane's constant offset.
+// Without it copies take 64-bit addresses, and zeros past the end of an activation row: four
+// to six more vector instructions for each (product of the training batch, 65536 x 4096 x
+// 6144: 1080 us so, 1072 us with FAST; gradient 2830 and 2755 us).
+template <int TM, int TN, bool FWD, bool FAST>
 struct Tile {
   static constexpr int BM = 64 * TM, BN = 64 * TN;
   static constexpr int DB = TN / 2;  // dgrad: MX blocks a lane decodes per step
@@ -244,7 +262,9 @@ struct Tile {
   const MxParams &p;
   Smem<TM, TN, FWD> &sm;
   int lane, w, wm, wn, nb, nk;
-  const uint8_t *asrc[2 * TM];  // activation rows of this lane's copies (bytes)
+  const uint8_t *asrc[FAST ? 1 : 2 * TM];  // activation rows of this lane's copies (bytes)
+  const uint8_t *abase;                    // FAST: what aoff counts from
+  uint32_t aoff[FAST ? 2 * TM : 1];
   int alen;                     // bytes of an activation row
   const uint8_t *zeros;
   const uint8_t *wbase;         // the expert's codes
@@ -254,6 +274,7 @@ struct Tile {
   u32x4 cc[DB];                 // dgrad: codes of the next step
   uint32_t sc[DB];              // and their scales
   int q0;                       // dgrad: first block of this wave
+  uint32_t coff[DB], soff[DB];  // dgrad, FAST: of codes and scales
   i32x4 af[2][TM], bf[2][TN];
   int ssa[TM], ssb[TN];         // forward: scale words of the step
   f32x16 acc[TM][TN];
@@ -278,19 +299,37 @@ struct Tile {
 #pragma unroll
     for (int j = 0; j < 2 * TM; ++j) {
       const int r = 8 * (2 * TM * w + j) + (lane >> 3);
+      const uint8_t *x = FWD ? p.xc : reinterpret_cast<const uint8_t *>(p.dy);
       const int64_t row = src_row(p, (int64_t)rb + min(m0 + r, n_e - 1));
-      asrc[j] = (FWD ? p.xc : reinterpret_cast<const uint8_t *>(p.dy)) + row * alen;
+      if constexpr (FAST) {
+        // without perm the rows follow each other: count from the tile's first
+        const int64_t row0 = p.perm ? 0 : src_row(p, (int64_t)rb + m0);
+        abase = x + row0 * alen;
+        aoff[j] = (uint32_t)((row - row0) * alen) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+      } else {
+        asrc[j] = x + row * alen;
+      }
     }
     wbase = p.wc + (int64_t)e * p.N * (p.K / 2);
     const uint8_t *ws = p.ws + (int64_t)e * p.N * nb;
     if constexpr (FWD) {
 #pragma unroll
-      for (int j = 0; j < 2 * TN; ++j) boff[j] = (uint32_t)min(n0 + 8 * (2 * TN * w + j) + (lane >> 3), p.N - 1) * (p.K / 2);
+      for (int j = 0; j < 2 * TN; ++j) {
+        const int r = 8 * (2 * TN * w + j) + (lane >> 3);
+        boff[j] = (uint32_t)min(n0 + r, p.N - 1) * (p.K / 2) + (FAST ? 16 * ((lane & 7) ^ ((r >> 1) & 7)) : 0);
+      }
       sb = ws + (int64_t)min(n0 + (tid < BN ? tid : 0), p.N - 1) * nb;
       sa = p.xs + src_row(p, (int64_t)rb + min(m0 + (tid < BM ? tid : 0), n_e - 1)) * nb;
     } else {
       sb = ws;
       q0 = n0 / 32 + w * DB;
+      if constexpr (FAST) {
+#pragma unroll
+        for (int i = 0; i < DB; ++i) {
+          coff[i] = (uint32_t)code_row(i) * (p.K / 2) + 16 * min(q0 + code_half(i), nb - 1);
+          soff[i] = (uint32_t)lane * nb + min(q0 + i, nb - 1);
+        }
+      }
     }
   }
 
@@ -298,15 +337,24 @@ struct Tile {
   // weights (any of the row's bytes there)
   __device__ __forceinline__ void copy(int j, int ks, int st) {
     if (j < 2 * TM) {
-      const int r = 8 * (2 * TM * w + j) + (lane >> 3);
-      const int o = 128 * ks + 16 * ((lane & 7) ^ ((r >> 1) & 7));
-      dma_b128(o < alen ? asrc[j] + o : zeros,
-               lds_addr(sm.a[st]) + 1024 * (2 * TM * w + j));
+      const uint32_t to = lds_addr(sm.a[st]) + 1024 * (2 * TM * w + j);
+      if constexpr (FAST) {
+        dma_b128(abase + 128 * ks, aoff[j], to);
+      } else {
+        const int r = 8 * (2 * TM * w + j) + (lane >> 3);
+        const int o = 128 * ks + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+        dma_b128(o < alen ? asrc[j] + o : zeros, to);
+      }
     } else if constexpr (FWD) {
       j -= 2 * TM;
-      const int r = 8 * (2 * TN * w + j) + (lane >> 3);
-      const int o = 128 * ks + 16 * ((lane & 7) ^ ((r >> 1) & 7));
-      dma_b128(wbase + (boff[j] + (uint32_t)(o < alen ? o : 0)), lds_addr(sm.b[st]) + 1024 * (2 * TN * w + j));
+      const uint32_t to = lds_addr(sm.b[st]) + 1024 * (2 * TN * w + j);
+      if constexpr (FAST) {
+        dma_b128(wbase + 128 * ks, boff[j], to);
+      } else {
+        const int r = 8 * (2 * TN * w + j) + (lane >> 3);
+        const int o = 128 * ks + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+        dma_b128(wbase + (boff[j] + (uint32_t)(o < alen ? o : 0)), to);
+      }
     }
   }
 
@@ -339,16 +387,29 @@ struct Tile {
   // The codes go to the wave's own LDS area two steps ahead (copies and not loads to
   // registers: the compiler would wait for those without counting the copies in between).
   // Row r keeps its half h of 32 bytes at h ^ (r >> 3 & 1) against bank conflicts.
+  __device__ __forceinline__ int code_row(int i) const { return (64 / DB) * i + lane / DB; }
+  __device__ __forceinline__ int code_half(int i) const {
+    return DB == 2 ? (lane & 1) ^ ((code_row(i) >> 3) & 1) : 0;
+  }
   __device__ __forceinline__ void code_op(int i, int ks) {
     const int d = ks & 1;
     if (i < DB) {
-      const int r = (64 / DB) * i + lane / DB, h = DB == 2 ? (lane & 1) ^ ((r >> 3) & 1) : 0;
-      const int64_t n = min(DK * ks + r, p.N - 1);  // past the end: the last row (its dY is zero)
-      const int q = min(q0 + h, nb - 1);            // past the end: columns that are dropped
-      dma_b128(wbase + n * (p.K / 2) + 16 * q, lds_addr(sm.c[d][w]) + 1024 * i);
+      const uint32_t to = lds_addr(sm.c[d][w]) + 1024 * i;
+      if constexpr (FAST) {  // (past the last step: its rows again, which nothing reads)
+        dma_b128(wbase + (int64_t)min(ks, nk - 1) * DK * (p.K / 2), coff[i], to);
+      } else {
+        const int64_t n = min(DK * ks + code_row(i), p.N - 1);  // past the end: the last row (its dY is zero)
+        const int q = min(q0 + code_half(i), nb - 1);           // past the end: columns that are dropped
+        dma_b128(wbase + n * (p.K / 2) + 16 * q, to);
+      }
     } else {
-      const int64_t n = min(DK * ks + lane, p.N - 1);
-      dma_u8(sb + n * nb + min(q0 + i - DB, nb - 1), lds_addr(sm.cs[d][w][i - DB]));
+      const uint32_t to = lds_addr(sm.cs[d][w][i - DB]);
+      if constexpr (FAST) {
+        dma_u8(sb + (int64_t)min(ks, nk - 1) * DK * nb, soff[i - DB], to);
+      } else {
+        const int64_t n = min(DK * ks + lane, p.N - 1);
+        dma_u8(sb + n * nb + min(q0 + i - DB, nb - 1), to);
+      }
     }
   }
   __device__ __forceinline__ void read_codes(int ks) {
@@ -615,7 +676,7 @@ struct Tile {
   }
 };
 
-template <int TM, int TN, bool FWD, int OCC>
+template <int TM, int TN, bool FWD, bool FAST, int OCC>
 __global__ void __launch_bounds__(NTHR, OCC) mx_tiles(MxParams p) {
   __shared__ __attribute__((aligned(16))) Smem<TM, TN, FWD> sm;
   constexpr int BM = 64 * TM, BN = 64 * TN;
@@ -626,7 +687,7 @@ __global__ void __launch_bounds__(NTHR, OCC) mx_tiles(MxParams p) {
   // flight there share an expert's rows and weights in its L2
   const int per = (total + 7) / 8;
   const int first = (blockIdx.x & 7) * per, last = min(first + per, total);
-  Tile<TM, TN, FWD> t(p, sm);
+  Tile<TM, TN, FWD, FAST> t(p, sm);
   for (int L = first + (int)(blockIdx.x >> 3); L < last; L += (int)(gridDim.x >> 3)) {
     const int mt = L / p.NT, n0 = (L % p.NT) * BN;
     map.find(mt, sm.found);
@@ -715,14 +776,18 @@ constexpr int64_t kBigRows = 96;
 
 template <bool FWD>
 bqm_status launch_tiles(MxParams p, hipStream_t s, const char *what) {
-  const int64_t ncols = FWD ? p.N : p.K;
+  const int64_t ncols = FWD ? p.N : p.K, alen = FWD ? p.K / 2 : 2 * (int64_t)p.N, most = (int64_t)1 << 32;
+  const bool fast = alen % 128 == 0 && (p.perm ? p.xrows : 256) * alen < most && (int64_t)p.N * (p.K / 2) < most;
   auto go = [&](auto TM, auto TN, auto OCC) {
     constexpr int BM = 64 * TM.value, BN = 64 * TN.value;
     p.NT = (int)cdiv(ncols, BN);
     // at most R / BM + E row tiles; as many workgroups as the chip holds at once
     const int64_t tiles = (p.R / BM + (p.E < p.R ? p.E : p.R)) * p.NT, slots = (int64_t)kCUs * OCC.value;
     const unsigned grid = (unsigned)(cdiv(tiles < slots ? tiles : slots, 8) * 8);
-    mx_tiles<TM.value, TN.value, FWD, OCC.value><<<grid, NTHR, 0, s>>>(p);
+    if (fast)
+      mx_tiles<TM.value, TN.value, FWD, true, OCC.value><<<grid, NTHR, 0, s>>>(p);
+    else
+      mx_tiles<TM.value, TN.value, FWD, false, OCC.value><<<grid, NTHR, 0, s>>>(p);
   };
   using std::integral_constant;
   if (p.R >= kBigRows * p.E)
