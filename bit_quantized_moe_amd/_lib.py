@@ -121,8 +121,9 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        # the current stream's handle without building a Stream object (0.1 us, not 2.8 us)
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -328,31 +329,44 @@ def bqm_lora_grad(d: MoEDesc, x, dy, ws, dA_gu, dB_gu, dA_dn, dB_dn, stream=None
 # tensors, so the tensors' types, shapes and layout are checked here; everything else is
 # checked behind the C ABI.
 # ----------------------------------------------------------------------------
-def _dense(name, t, dtype, shape=None):
-    """t (None passes) if it is a contiguous tensor of that dtype and number of elements."""
+def _dense(name, t, dtype, *shape):
+    """t (None passes) if it is a contiguous GPU tensor of that dtype and number of elements."""
     if t is None:
         return None
-    import torch
-    if t.dtype is not getattr(torch, dtype):
+    if t.dtype is not _dtype(dtype):
         raise BQMError(-1, f"{name}: dtype {t.dtype}, torch.{dtype} needed")
     if not t.is_contiguous():
         raise BQMError(-2, f"{name}: not contiguous")
-    if shape is not None and t.numel() != math.prod(shape):
-        raise BQMError(-2, f"{name}: shape {tuple(t.shape)}, {tuple(shape)} needed")
+    if shape and t.numel() != math.prod(shape):
+        raise BQMError(-2, f"{name}: shape {tuple(t.shape)}, {shape} needed")
+    if t.get_device() < 0:
+        raise BQMError(-1, f"{name}: not a GPU tensor")
     return t
 
 
-def _dense_q(name, q: QTensor, blk=32):
-    _dense(name + ".codes", q.codes, "uint8", (q.n_mat, q.rows, q.cols // 2))
-    _dense(name + ".scales", q.scales, "uint8", (q.n_mat, q.rows, q.cols // blk))
+_dtypes = {}
+
+
+def _dtype(name):
+    if name not in _dtypes:
+        import torch
+        _dtypes[name] = getattr(torch, name)
+    return _dtypes[name]
+
+
+def _mxfp4(name, q: QTensor):
+    if q.fmt != FMT_MXFP4:
+        raise BQMError(-1, f"{name}: format {q.fmt}, FMT_MXFP4 needed")
+    _dense(name + ".codes", q.codes, "uint8", q.n_mat, q.rows, q.cols // 2)
+    _dense(name + ".scales", q.scales, "uint8", q.n_mat, q.rows, q.cols // 32)
     return q.c()
 
 
 def bqm_quantize_mxfp4(x, out: QTensor, stream=None):
     """bf16 x [n_mat, rows, cols] -> out, an MXFP4 stack (returned)."""
     lib = load()
-    _dense("x", x, "bfloat16", (out.n_mat, out.rows, out.cols))
-    qc = _dense_q("out", out)
+    _dense("x", x, "bfloat16", out.n_mat, out.rows, out.cols)
+    qc = _mxfp4("out", out)
     _check(lib.bqm_quantize_mxfp4(_ptr(x), C.byref(qc), _stream(stream)))
     return out
 
@@ -362,10 +376,10 @@ def bqm_mxfp4_gemm(x: QTensor, w: QTensor, offsets, perm, k, y, stream=None):
     are in routed order already.  R is y's first dimension."""
     lib = load()
     R = y.shape[0]
-    xc, wc = _dense_q("x", x), _dense_q("w", w)
-    _dense("offsets", offsets, "int32", (w.n_mat + 1,))
-    _dense("perm", perm, "int32", (R,))
-    _dense("y", y, "bfloat16", (R, w.rows))
+    xc, wc = _mxfp4("x", x), _mxfp4("w", w)
+    _dense("offsets", offsets, "int32", w.n_mat + 1)
+    _dense("perm", perm, "int32", R)
+    _dense("y", y, "bfloat16", R, w.rows)
     _check(lib.bqm_mxfp4_gemm(C.byref(xc), C.byref(wc), _ptr(offsets), _ptr(perm), k, R, _ptr(y), _stream(stream)))
     return y
 
@@ -374,11 +388,11 @@ def bqm_mxfp4_dgrad(w: QTensor, dy, offsets, perm, k, dx, stream=None):
     """dx [R, K] = rows of dy [rows, N] times their experts' DQ(w) [E, N, K]."""
     lib = load()
     R = dx.shape[0]
-    wc = _dense_q("w", w)
-    _dense("dy", dy, "bfloat16", (dy.shape[0], w.rows))
-    _dense("offsets", offsets, "int32", (w.n_mat + 1,))
-    _dense("perm", perm, "int32", (R,))
-    _dense("dx", dx, "bfloat16", (R, w.cols))
+    wc = _mxfp4("w", w)
+    _dense("dy", dy, "bfloat16", dy.shape[0], w.rows)
+    _dense("offsets", offsets, "int32", w.n_mat + 1)
+    _dense("perm", perm, "int32", R)
+    _dense("dx", dx, "bfloat16", R, w.cols)
     _check(lib.bqm_mxfp4_dgrad(C.byref(wc), _ptr(dy), dy.shape[0], _ptr(offsets), _ptr(perm), k, R, _ptr(dx),
                                _stream(stream)))
     return dx
@@ -389,12 +403,12 @@ def bqm_swiglu_ckpt_fwd(h, h8, h8_scales, a=None, aq: Optional[QTensor] = None, 
     where given.  n_rows: a one-element int32 tensor (offsets[E:], say)."""
     lib = load()
     R, I = h.shape[0], h.shape[1] // 2
-    _dense("h", h, "bfloat16", (R, 2 * I))
-    _dense("h8", h8, "uint8", (R, 2 * I))
-    _dense("h8_scales", h8_scales, "uint8", (R, 2 * I // 32))
-    _dense("a", a, "bfloat16", (R, I))
-    _dense("n_rows", n_rows, "int32", (1,))
-    qc = None if aq is None else C.byref(_dense_q("aq", aq))
+    _dense("h", h, "bfloat16", R, 2 * I)
+    _dense("h8", h8, "uint8", R, 2 * I)
+    _dense("h8_scales", h8_scales, "uint8", R, 2 * I // 32)
+    _dense("a", a, "bfloat16", R, I)
+    _dense("n_rows", n_rows, "int32", 1)
+    qc = None if aq is None else C.byref(_mxfp4("aq", aq))
     _check(lib.bqm_swiglu_ckpt_fwd(_ptr(h), R, I, _ptr(n_rows), _ptr(h8), _ptr(h8_scales), _ptr(a), qc,
                                    _stream(stream)))
 
@@ -403,14 +417,14 @@ def bqm_swiglu_ckpt_bwd(h8, h8_scales, da, perm, topk_w, dh, dtopk_w=None, n_row
     """The 8-bit copy and da [R, I] -> dh [R, 2I], dtopk_w [R] (or [T, k]) where given."""
     lib = load()
     R, I = da.shape
-    _dense("h8", h8, "uint8", (R, 2 * I))
-    _dense("h8_scales", h8_scales, "uint8", (R, 2 * I // 32))
-    _dense("da", da, "bfloat16", (R, I))
-    _dense("perm", perm, "int32", (R,))
-    _dense("topk_w", topk_w, "float32", (R,))
-    _dense("dh", dh, "bfloat16", (R, 2 * I))
-    _dense("dtopk_w", dtopk_w, "float32", (R,))
-    _dense("n_rows", n_rows, "int32", (1,))
+    _dense("h8", h8, "uint8", R, 2 * I)
+    _dense("h8_scales", h8_scales, "uint8", R, 2 * I // 32)
+    _dense("da", da, "bfloat16", R, I)
+    _dense("perm", perm, "int32", R)
+    _dense("topk_w", topk_w, "float32", R)
+    _dense("dh", dh, "bfloat16", R, 2 * I)
+    _dense("dtopk_w", dtopk_w, "float32", R)
+    _dense("n_rows", n_rows, "int32", 1)
     _check(lib.bqm_swiglu_ckpt_bwd(_ptr(h8), _ptr(h8_scales), _ptr(da), _ptr(perm), _ptr(topk_w), R, I, _ptr(n_rows),
                                    _ptr(dh), _ptr(dtopk_w), _stream(stream)))
     return dh
@@ -426,10 +440,10 @@ def bqm_router_loss(logits, topk_idx, valid, counts, loss, ws, stream=None):
     lib = load()
     (T, E), k = logits.shape, topk_idx.shape[1]
     _dense("logits", logits, "float32")
-    _dense("topk_idx", topk_idx, "int32", (T, k))
-    _dense("valid", valid, "uint8", (T,))
-    _dense("counts", counts, "int32", (E + 1,))
-    _dense("loss", loss, "float32", (2,))
+    _dense("topk_idx", topk_idx, "int32", T, k)
+    _dense("valid", valid, "uint8", T)
+    _dense("counts", counts, "int32", E + 1)
+    _dense("loss", loss, "float32", 2)
     wsb = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib.bqm_router_loss(_ptr(logits), _ptr(topk_idx), _ptr(valid), T, E, k, _ptr(counts), _ptr(loss), _ptr(ws),
                                wsb, _stream(stream)))
@@ -441,12 +455,12 @@ def bqm_router_grad(logits, topk_idx, valid, counts, dtopk_w, dloss, renorm, dlo
     lib = load()
     (T, E), k = logits.shape, topk_idx.shape[1]
     _dense("logits", logits, "float32")
-    _dense("topk_idx", topk_idx, "int32", (T, k))
-    _dense("valid", valid, "uint8", (T,))
-    _dense("counts", counts, "int32", (E + 1,))
-    _dense("dtopk_w", dtopk_w, "float32", (T, k))
-    _dense("dloss", dloss, "float32", (2,))
-    _dense("dlogits", dlogits, "float32", (T, E))
+    _dense("topk_idx", topk_idx, "int32", T, k)
+    _dense("valid", valid, "uint8", T)
+    _dense("counts", counts, "int32", E + 1)
+    _dense("dtopk_w", dtopk_w, "float32", T, k)
+    _dense("dloss", dloss, "float32", 2)
+    _dense("dlogits", dlogits, "float32", T, E)
     _check(lib.bqm_router_grad(_ptr(logits), _ptr(topk_idx), _ptr(valid), _ptr(counts), _ptr(dtopk_w), _ptr(dloss), T,
                                E, k, int(renorm), _ptr(dlogits), _stream(stream)))
     return dlogits

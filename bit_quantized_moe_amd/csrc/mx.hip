@@ -182,21 +182,21 @@ __device__ __forceinline__ int64_t src_row(const MxParams &p, int64_t pos) {
 constexpr int DK = 64;   // dgrad: weight rows per step
 constexpr int DQS = 72;  // dgrad: row stride (bf16) of a decoded 64-column group
 
-template <int TM, int TN, bool FWD>
+template <int TM, int TN, bool FWD, int NS>
 struct Smem;
 template <int TM, int TN>
-struct Smem<TM, TN, true> {
+struct Smem<TM, TN, true, 2> {
   uint8_t a[2][64 * TM * 128];
   uint8_t b[2][64 * TN * 128];
   uint32_t s[2][2][2][64 * (TM + TN) + 4];  // [group parity][step of the group][half][row]
   int wsum[NTHR / 64], found[2];
 };
-template <int TM, int TN>
-struct Smem<TM, TN, false> {
-  uint8_t a[2][64 * TM * 128];
+template <int TM, int TN, int NS>
+struct Smem<TM, TN, false, NS> {
+  uint8_t a[NS][64 * TM * 128];
   uint16_t dq[2][TN][DK * DQS];
-  uint8_t c[2][NTHR / 64][DK * 16 * (TN / 2)];  // each wave's codes of a step: 64 rows of its blocks
-  uint32_t cs[2][NTHR / 64][TN / 2][DK];        // and their scales
+  uint8_t c[NS][NTHR / 64][DK * 16 * (TN / 2)];  // each wave's codes of a step: 64 rows of its blocks
+  uint32_t cs[NS][NTHR / 64][TN / 2][DK];        // and their scales
   int wsum[NTHR / 64], found[2];
 };
 
@@ -254,13 +254,19 @@ __device__ __forceinline__ float e8m0(uint32_t c) {
 // Without it copies take 64-bit addresses, and zeros past the end of an activation row: four
 // to six more vector instructions for each (product of the training batch, 65536 x 4096 x
 // 6144: 1080 us so, 1072 us with FAST; gradient 2830 and 2755 us).
-template <int TM, int TN, bool FWD, bool FAST>
+// NS: stages.  Two: the copies of a step begin in slice 3 of the step before the last.  Four
+// (the gradient with few rows, where the activation stages are small): they run three steps
+// ahead, which a stream of weights from HBM needs when a step holds little else.
+template <int TM, int TN, bool FWD, bool FAST, int NS>
 struct Tile {
   static constexpr int BM = 64 * TM, BN = 64 * TN;
   static constexpr int DB = TN / 2;  // dgrad: MX blocks a lane decodes per step
-  static constexpr int kCodeOps = 2 * DB;  // dgrad: copies of codes and of scales per step
+  static constexpr int kCodeOps = FWD ? 0 : 2 * DB;  // dgrad: copies of codes and of scales per step
+  static constexpr bool DEEP = NS > 2;
+  static constexpr int D = NS - 1;  // DEEP: steps the copies run ahead
+  static_assert(!DEEP || !FWD, "the forward's scales are loaded one group ahead");
   const MxParams &p;
-  Smem<TM, TN, FWD> &sm;
+  Smem<TM, TN, FWD, NS> &sm;
   int lane, w, wm, wn, nb, nk;
   const uint8_t *asrc[FAST ? 1 : 2 * TM];  // activation rows of this lane's copies (bytes)
   const uint8_t *abase;                    // FAST: what aoff counts from
@@ -279,7 +285,7 @@ struct Tile {
   int ssa[TM], ssb[TN];         // forward: scale words of the step
   f32x16 acc[TM][TN];
 
-  __device__ __forceinline__ Tile(const MxParams &p_, Smem<TM, TN, FWD> &sm_) : p(p_), sm(sm_) {
+  __device__ __forceinline__ Tile(const MxParams &p_, Smem<TM, TN, FWD, NS> &sm_) : p(p_), sm(sm_) {
     lane = threadIdx.x & 63;
     w = wave_id();
     wm = w >> 1;
@@ -339,7 +345,8 @@ struct Tile {
     if (j < 2 * TM) {
       const uint32_t to = lds_addr(sm.a[st]) + 1024 * (2 * TM * w + j);
       if constexpr (FAST) {
-        dma_b128(abase + 128 * ks, aoff[j], to);
+        // (DEEP: past the last step its bytes again, which nothing reads)
+        dma_b128(abase + 128 * (DEEP ? min(ks, nk - 1) : ks), aoff[j], to);
       } else {
         const int r = 8 * (2 * TM * w + j) + (lane >> 3);
         const int o = 128 * ks + 16 * ((lane & 7) ^ ((r >> 1) & 7));
@@ -392,7 +399,7 @@ struct Tile {
     return DB == 2 ? (lane & 1) ^ ((code_row(i) >> 3) & 1) : 0;
   }
   __device__ __forceinline__ void code_op(int i, int ks) {
-    const int d = ks & 1;
+    const int d = ks & (NS - 1);
     if (i < DB) {
       const uint32_t to = lds_addr(sm.c[d][w]) + 1024 * i;
       if constexpr (FAST) {  // (past the last step: its rows again, which nothing reads)
@@ -413,7 +420,7 @@ struct Tile {
     }
   }
   __device__ __forceinline__ void read_codes(int ks) {
-    const int d = ks & 1;
+    const int d = ks & (NS - 1);
 #pragma unroll
     for (int b = 0; b < DB; ++b) {
       const int h = DB == 2 ? b ^ ((lane >> 3) & 1) : 0;
@@ -429,6 +436,9 @@ struct Tile {
                      fp4_bf16<3>(cc[b][i], f)};
     *reinterpret_cast<u32x4 *>(sm.dq[d][blk >> 1] + lane * DQS + 32 * (blk & 1) + 8 * i) = o;
   }
+
+  // stage of the activations of step ks, of parity st
+  __device__ __forceinline__ static int stage(int ks, int st) { return DEEP ? ks & (NS - 1) : st; }
 
   // ---- fragments of slice kk of stage st into set k ----
   __device__ __forceinline__ void read_a(int k, int tm, int kk, int st) {
@@ -457,13 +467,14 @@ struct Tile {
   // The copies of step ks + 2 go into the stage that step ks has finished reading: the first
   // half from slice 3 of step ks on (after its barrier), the rest in slice 0 of step ks + 1.
   // LEFT: steps that follow (0, 1, or 2 for more).  PAR: the step's parity (-1: not known).
-  static constexpr int kCopies = 2 * TM + (FWD ? 2 * TN : 0), kFirst = kCopies / 2;
+  static constexpr int kCopies = 2 * TM + (FWD ? 2 * TN : 0), kFirst = DEEP ? 0 : kCopies / 2;
+  static constexpr int kOps = kCopies + kCodeOps;  // per step
 
   // Copies of this wave that its wait in slice 3 may leave in flight: those for later steps
   // than the next
   template <int LEFT>
   static constexpr int in_flight() {
-    return !FWD && LEFT > 1 ? kCodeOps : 0;
+    return DEEP ? (D - 1) * kOps : (LEFT > 1 ? kCodeOps : 0);
   }
 
   // other work of slices 0-2, item i: fragment reads of the next slice, then copies and what
@@ -475,7 +486,7 @@ struct Tile {
   static constexpr int items() {
     const int reads = TN + VT;
     if (LEFT == 0) return reads;
-    if (KK == 0) return reads + (kCopies - kFirst) + (FWD ? (PAR == 0 ? 1 : 0) : in_flight<LEFT>());
+    if (KK == 0) return reads + (kCopies - kFirst) + (FWD ? (PAR == 0 ? 1 : 0) : (DEEP || LEFT > 1 ? kCodeOps : 0));
     if (KK == 1) return reads + (FWD ? 0 : 1 + 2 * DB);
     return reads + (FWD ? 1 : 2 * DB);
   }
@@ -484,24 +495,28 @@ struct Tile {
     constexpr int k = (KK + 1) & 1;
     if (i < TN) return read_b(k, i, KK + 1, st);
     i -= TN;
-    if (i < VT) return read_a(k, i, KK + 1, st);
+    if (i < VT) return read_a(k, i, KK + 1, stage(ks, st));
     i -= VT;
     if constexpr (LEFT > 0) {
       if constexpr (KK == 0) {
-        if (i < kCopies - kFirst) return copy(kFirst + i, ks + 1, st ^ 1);
+        // (DEEP: stage ks + D was read in step ks - 1)
+        constexpr int ahead = DEEP ? D : 1;
+        if (i < kCopies - kFirst) return copy(kFirst + i, ks + ahead, stage(ks + ahead, st ^ 1));
         i -= kCopies - kFirst;
         if constexpr (FWD) {
           // the next group, or the last again (it is then not used)
           get_scales(min((ks >> 1) + 1, (nb - 1) >> 4));
         } else {
-          code_op(i, ks + 2);
+          code_op(i, ks + (DEEP ? D : 2));
         }
       } else if constexpr (KK == 1) {
         if constexpr (!FWD) {
           if (i == 0) {
             // this wave's codes of the next step, older than the copies of the step after
             // it (the first kFirst) and than what slice 0 issued
-            if constexpr (LEFT > 1)
+            if constexpr (DEEP)
+              wait_vm<(D - 1) * kOps>();
+            else if constexpr (LEFT > 1)
               wait_vm<kCopies + kCodeOps>();
             else
               wait_vm<kCopies - kFirst>();
@@ -536,7 +551,7 @@ struct Tile {
   // and the copies of the step after it begin
   template <int VT, int LEFT>
   __device__ __forceinline__ void slice3(int ks, int st) {
-    constexpr int NP = VT * TN, NR = TN + VT, NW = FWD ? NR : 0, NI = NR + NW + (LEFT > 1 ? kFirst : 0);
+    constexpr int NP = VT * TN, NR = TN + VT, NW = FWD ? NR : 0, NI = NR + NW + (LEFT > 1 && !DEEP ? kFirst : 0);
     int na[TM], nw[TN];
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
@@ -556,7 +571,7 @@ struct Tile {
           if (i < TN)
             read_b(0, i, 0, st ^ 1);
           else if (i < NR)
-            read_a(0, i - TN, 0, st ^ 1);
+            read_a(0, i - TN, 0, stage(ks + 1, st ^ 1));
           else if (i < NR + NW) {
             const int j = i - NR;
             if (j < TN)
@@ -602,23 +617,32 @@ struct Tile {
         va = load_few_scales(sa, nb);
         vb = load_few_scales(sb, nb);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kCodeOps; ++i) code_op(i, 0);
     }
 #pragma unroll
-    for (int j = 0; j < kCopies; ++j) copy(j, 0, 0);
+    for (int q = 0; q < (DEEP ? D : 1); ++q) {
+      if constexpr (!FWD) {
+#pragma unroll
+        for (int i = 0; i < kCodeOps; ++i) code_op(i, q);
+      }
+#pragma unroll
+      for (int j = 0; j < kCopies; ++j) copy(j, q, q);
+    }
     if constexpr (FWD) {
       put_scales(0);
     } else {
-      wait_vm<kCopies>();  // this wave's codes
+      if constexpr (DEEP)
+        wait_vm<(D - 1) * kOps>();  // step 0's
+      else
+        wait_vm<kCopies>();  // this wave's codes
       read_codes(0);
 #pragma unroll
       for (int u = 0; u < 4 * DB; ++u) decode(u, 0);
+      if constexpr (!DEEP) {
 #pragma unroll
-      for (int i = 0; i < kCodeOps; ++i) code_op(i, 1);
+        for (int i = 0; i < kCodeOps; ++i) code_op(i, 1);
+      }
     }
-    wait_vm<0>();
+    if constexpr (!DEEP) wait_vm<0>();
     barrier_lds();
 #pragma unroll
     for (int tn = 0; tn < TN; ++tn) read_b(0, tn, 0, 0);
@@ -631,7 +655,7 @@ struct Tile {
 #pragma unroll
       for (int tm = 0; tm < VT; ++tm) ssa[tm] = (int)sw[32 * (2 * tm + wm) + (lane & 31)];
     }
-    if (nk > 1) {
+    if (!DEEP && nk > 1) {
 #pragma unroll
       for (int j = 0; j < kFirst; ++j) copy(j, 1, 1);
     }
@@ -646,6 +670,7 @@ struct Tile {
       ++ks;
     }
     step<VT, 0, -1>(ks, ks & 1);
+    if constexpr (DEEP) wait_vm<0>();  // the copies of no step, before the next tile's take their stages
   }
 
   // rows: those of the tile that exist; ncols: columns of the output
@@ -676,9 +701,9 @@ struct Tile {
   }
 };
 
-template <int TM, int TN, bool FWD, bool FAST, int OCC>
+template <int TM, int TN, bool FWD, bool FAST, int OCC, int NS>
 __global__ void __launch_bounds__(NTHR, OCC) mx_tiles(MxParams p) {
-  __shared__ __attribute__((aligned(16))) Smem<TM, TN, FWD> sm;
+  __shared__ __attribute__((aligned(16))) Smem<TM, TN, FWD, NS> sm;
   constexpr int BM = 64 * TM, BN = 64 * TN;
   const int ncols = FWD ? p.N : p.K;
   TileMap map;
@@ -687,7 +712,7 @@ __global__ void __launch_bounds__(NTHR, OCC) mx_tiles(MxParams p) {
   // flight there share an expert's rows and weights in its L2
   const int per = (total + 7) / 8;
   const int first = (blockIdx.x & 7) * per, last = min(first + per, total);
-  Tile<TM, TN, FWD, FAST> t(p, sm);
+  Tile<TM, TN, FWD, FAST, NS> t(p, sm);
   for (int L = first + (int)(blockIdx.x >> 3); L < last; L += (int)(gridDim.x >> 3)) {
     const int mt = L / p.NT, n0 = (L % p.NT) * BN;
     map.find(mt, sm.found);
@@ -772,28 +797,38 @@ bqm_status check_routed(const char *who, const bqm_qtensor *w, const int32_t *of
 constexpr int kCUs = 256;
 
 // Tile size by the rows an expert has on average (the host knows R and E, not the offsets).
-constexpr int64_t kBigRows = 96;
+// Measured with N = 2816 (gradient: 2048) and K = 2048 over 60 (64) experts, us at 16, 64,
+// 100, 160 and 256 rows (gradient: 12, 64, 128 and 256) an expert:
+//   product   64 x 128: 44 54 68 91 119    128 x 128: 46 55 63 83 97    256 x 256: 54 61 68 77 94
+//   gradient  64 x 256: @DG@               256 x 256: 72 74 88 132
+constexpr int64_t kFewRows = 64, kManyRows = 128, kManyRowsDgrad = 96;
 
 template <bool FWD>
 bqm_status launch_tiles(MxParams p, hipStream_t s, const char *what) {
   const int64_t ncols = FWD ? p.N : p.K, alen = FWD ? p.K / 2 : 2 * (int64_t)p.N, most = (int64_t)1 << 32;
   const bool fast = alen % 128 == 0 && (p.perm ? p.xrows : 256) * alen < most && (int64_t)p.N * (p.K / 2) < most;
-  auto go = [&](auto TM, auto TN, auto OCC) {
+  auto go = [&](auto TM, auto TN, auto OCC, auto NS) {
     constexpr int BM = 64 * TM.value, BN = 64 * TN.value;
     p.NT = (int)cdiv(ncols, BN);
     // at most R / BM + E row tiles; as many workgroups as the chip holds at once
     const int64_t tiles = (p.R / BM + (p.E < p.R ? p.E : p.R)) * p.NT, slots = (int64_t)kCUs * OCC.value;
     const unsigned grid = (unsigned)(cdiv(tiles < slots ? tiles : slots, 8) * 8);
     if (fast)
-      mx_tiles<TM.value, TN.value, FWD, true, OCC.value><<<grid, NTHR, 0, s>>>(p);
+      mx_tiles<TM.value, TN.value, FWD, true, OCC.value, NS.value><<<grid, NTHR, 0, s>>>(p);
     else
-      mx_tiles<TM.value, TN.value, FWD, false, OCC.value><<<grid, NTHR, 0, s>>>(p);
+      mx_tiles<TM.value, TN.value, FWD, false, OCC.value, NS.value><<<grid, NTHR, 0, s>>>(p);
   };
-  using std::integral_constant;
-  if (p.R >= kBigRows * p.E)
-    go(integral_constant<int, 4>{}, integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  constexpr std::integral_constant<int, 1> one;
+  constexpr std::integral_constant<int, 2> two;
+  constexpr std::integral_constant<int, 4> four;
+  if (p.R >= (FWD ? kManyRows : kManyRowsDgrad) * p.E)
+    go(four, four, one, two);
+  else if constexpr (!FWD)
+    go(one, four, one, four);
+  else if (p.R >= kFewRows * p.E)
+    go(two, two, two, two);
   else
-    go(integral_constant<int, 1>{}, integral_constant<int, 2>{}, integral_constant<int, 2>{});
+    go(one, two, two, two);
   return launch_status(what);
 }
 

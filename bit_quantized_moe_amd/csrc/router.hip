@@ -24,21 +24,38 @@ namespace bqm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 constexpr int kMaxE = 1024, kMaxK = 16;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // Reductions over groups of L lanes (a power of two); every lane gets the result.  Within
-// 16 lanes by DPP moves, beyond that by cross-lane shuffles.
+// 16 lanes by DPP moves, beyond that by exchanging rows of 16 and halves of the wave: vector
+// instructions all, none of which waits for the LDS crossbar as a shuffle does.
+__device__ __forceinline__ void swap_rows16(float v, float &a, float &b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void swap_halves(float v, float &a, float &b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
 template <int L, class F>
 __device__ __forceinline__ float group_reduce(float v, F op) {
   if constexpr (L >= 2) v = op(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, false)));
   if constexpr (L >= 4) v = op(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, false)));
   if constexpr (L >= 8) v = op(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, false)));
   if constexpr (L >= 16) v = op(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, false)));
-  if constexpr (L >= 32) v = op(v, __shfl_xor(v, 16, 64));
-  if constexpr (L >= 64) v = op(v, __shfl_xor(v, 32, 64));
+  float a, b;
+  if constexpr (L >= 32) {
+    swap_rows16(v, a, b);
+    v = op(a, b);
+  }
+  if constexpr (L >= 64) {
+    swap_halves(v, a, b);
+    v = op(a, b);
+  }
   return v;
 }
 template <int L>
@@ -67,6 +84,19 @@ __device__ __forceinline__ int expert_of(int v, int c, int l) {
   return VEC ? 4 * (v * L + l) + c : (4 * v + c) * L + l;
 }
 
+// orders this wave's LDS accesses for the compiler (the hardware keeps their order)
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// where expert e sits in the order (v, l, c) of the lanes' vectors without 16-byte loads
+template <int L, int NV>
+__device__ __forceinline__ int slot_of(int e) {
+  const int l = e & (L - 1), q = e / L;  // q = 4 v + c
+  return 4 * ((q >> 2) * L + l) + (q & 3);
+}
+
 template <int L, int NV, bool VEC>
 __device__ __forceinline__ void load_row(const float *__restrict__ row, int E, int l, bool use, f32x4 (&x)[NV]) {
 #pragma unroll
@@ -85,15 +115,15 @@ __device__ __forceinline__ void load_row(const float *__restrict__ row, int E, i
   }
 }
 
-// x <- e^(x - max); returns 1 / sum (0 for a row of nothing but -inf) and the row's lse
-// (0 for such a row)
+// x <- e^(x - base), base the row's maximum (0 for a row of nothing but -inf); returns 1 / sum
+// and the row's lse (both 0 for such a row)
 template <int L, int NV>
-__device__ __forceinline__ float softmax_row(f32x4 (&x)[NV], float &lse) {
+__device__ __forceinline__ float softmax_row(f32x4 (&x)[NV], float &lse, float &base) {
   float m = -INFINITY;
 #pragma unroll
   for (int v = 0; v < NV; ++v) m = fmaxf(m, fmaxf(fmaxf(x[v][0], x[v][1]), fmaxf(x[v][2], x[v][3])));
   m = group_max<L>(m);
-  const float base = m == -INFINITY ? 0.0f : m;
+  base = m == -INFINITY ? 0.0f : m;
   float s = 0.0f;
 #pragma unroll
   for (int v = 0; v < NV; ++v)
@@ -129,9 +159,11 @@ struct LossGeom {
   size_t bytes;
 };
 
-// Tokens per workgroup at least kTokMin, so that a small batch writes few partial sums;
-// at most 512 workgroups (two of 4 waves per CU keep the row loads in flight).
-constexpr int64_t kTokMin = 32;
+// Workgroups of 16 waves, two per CU at most: 32 waves keep enough rows in flight (with 8
+// waves per CU the 131072 x 256 batch took 62 us, @S@ us so).  A workgroup takes at least
+// kTokMin tokens, so that a small batch writes few partial sums.
+constexpr int kSumThreads = 1024, kSumWaves = kSumThreads / 64;
+constexpr int64_t kTokMin = 64;
 LossGeom loss_geom(int64_t T, int32_t E) {
   int64_t G = cdiv(T, kTokMin);
   G = G < 1 ? 1 : (G > 512 ? 512 : G);
@@ -159,36 +191,52 @@ LossWs loss_ws(void *ws, int G, int E) {
 }
 
 template <int L, int NV, bool VEC>
-__global__ void __launch_bounds__(kThreads) router_sums(const float *__restrict__ logits,
+__global__ void __launch_bounds__(kSumThreads) router_sums(const float *__restrict__ logits,
                                                         const int32_t *__restrict__ idx,
                                                         const uint8_t *__restrict__ valid, int64_t T, int E, int k,
                                                         LossWs w) {
-  constexpr int kGroups = kThreads / L;
-  __shared__ float ps[kMaxE];
+  constexpr int kGroups = kSumThreads / L;
+  extern __shared__ float ps[];  // [kSumWaves][E]: the waves' sums
   __shared__ int32_t hist[kMaxE];
-  __shared__ float zs[kWaves];
-  __shared__ int32_t ns[kWaves];
-  const int tid = threadIdx.x, l = tid & (L - 1), grp = tid / L, wave = tid >> 6, lane = tid & 63;
-  for (int e = tid; e < E; e += kThreads) {
-    ps[e] = 0.0f;
-    hist[e] = 0;
-  }
+  __shared__ float zs[kSumWaves];
+  __shared__ int32_t ns[kSumWaves];
+  const int tid = threadIdx.x, l = tid & (L - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int grp = L == 64 ? wave : tid / L;
+  for (int e = tid; e < E; e += kSumThreads) hist[e] = 0;
   if (blockIdx.x == 0 && tid == 0) *w.arrived = 0u;
   __syncthreads();
   f32x4 acc[NV] = {};
   float z = 0.0f;
   int32_t n = 0;
-  for (int64_t t = (int64_t)blockIdx.x * kGroups + grp; t < T; t += (int64_t)gridDim.x * kGroups) {
-    const bool use = !valid || valid[t];
-    f32x4 x[NV];
-    load_row<L, NV, VEC>(logits + t * E, E, l, use, x);
-    if (use)
-      for (int j = l; j < k; j += L) {
+  const int64_t step = (int64_t)gridDim.x * kGroups;
+  int64_t t = (int64_t)blockIdx.x * kGroups + grp;
+  // the next token's row, flag and index are loaded while this one's are reduced
+  f32x4 x[NV], nx[NV];
+  bool use = false, nuse = false;
+  int ix = -1, nix = -1;
+  auto fetch = [&](int64_t tt) {
+    nuse = !valid || valid[tt];
+    load_row<L, NV, VEC>(logits + tt * E, E, l, true, nx);
+    nix = l < k ? idx[tt * k + l] : -1;
+  };
+  if (t < T) fetch(t);
+  for (; t < T; t += step) {
+    use = nuse;
+    ix = nix;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[v][c] = use ? nx[v][c] : -INFINITY;
+    if (t + step < T) fetch(t + step);
+    if (use) {
+      if ((unsigned)ix < (unsigned)E) atomicAdd(&hist[ix], 1);
+      for (int j = l + L; j < k; j += L) {  // groups of fewer lanes than k
         const int e = idx[t * k + j];
         if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
       }
-    float lse;
-    const float inv = softmax_row<L, NV>(x, lse);
+    }
+    float lse, base;
+    const float inv = softmax_row<L, NV>(x, lse, base);
 #pragma unroll
     for (int v = 0; v < NV; ++v) acc[v] += x[v] * inv;
     if (use && l == 0) {
@@ -212,26 +260,27 @@ __global__ void __launch_bounds__(kThreads) router_sums(const float *__restrict_
     zs[wave] = z;
     ns[wave] = n;
   }
-  for (int q = 0; q < kWaves; ++q) {
-    if (wave == q && lane < L) {
+  if (lane < L) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int e = expert_of<L, NV, VEC>(v, c, l);
-          if (e < E) ps[e] += acc[v][c];
-        }
-    }
-    __syncthreads();
+      for (int c = 0; c < 4; ++c) {
+        const int e = expert_of<L, NV, VEC>(v, c, l);
+        if (e < E) ps[wave * E + e] = acc[v][c];
+      }
   }
-  for (int e = tid; e < E; e += kThreads) {
-    w.psum[(int64_t)blockIdx.x * E + e] = ps[e];
+  __syncthreads();
+  for (int e = tid; e < E; e += kSumThreads) {
+    float p = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kSumWaves; ++q) p += ps[q * E + e];
+    w.psum[(int64_t)blockIdx.x * E + e] = p;
     w.counts[(int64_t)blockIdx.x * E + e] = hist[e];
   }
   if (tid == 0) {
     float zt = 0.0f;
     int32_t nt = 0;
-    for (int q = 0; q < kWaves; ++q) {
+    for (int q = 0; q < kSumWaves; ++q) {
       zt += zs[q];
       nt += ns[q];
     }
@@ -243,9 +292,9 @@ __global__ void __launch_bounds__(kThreads) router_sums(const float *__restrict_
 // Workgroup b adds the G partial sums of experts kFinE b .. in FP64 and forms their share
 // sum_e c_e P_e; the workgroup that arrives last adds the shares in order.  (The counter is
 // cleared by the first kernel of the same call, so a workspace needs no preparation.)
-constexpr int kFinParts = kThreads / kFinE;
+constexpr int kFinThreads = 1024, kFinParts = kFinThreads / kFinE;
 
-__global__ void __launch_bounds__(kThreads) router_finish(LossWs w, int G, int E, int k, int32_t *__restrict__ counts,
+__global__ void __launch_bounds__(kFinThreads) router_finish(LossWs w, int G, int E, int k, int32_t *__restrict__ counts,
                                                           float *__restrict__ loss) {
   __shared__ double ps[kFinParts][kFinE];
   __shared__ int32_t cs[kFinParts][kFinE];
@@ -255,6 +304,7 @@ __global__ void __launch_bounds__(kThreads) router_finish(LossWs w, int G, int E
   double p = 0.0;
   int32_t c = 0;
   if (e < E)
+#pragma unroll 4
     for (int g = part; g < G; g += kFinParts) {
       p += (double)w.psum[(int64_t)g * E + e];
       c += w.counts[(int64_t)g * E + e];
@@ -284,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) router_finish(LossWs w, int G, int E
   // the last workgroup: tokens and lse^2 over the G partial sums, then the losses
   double z = 0.0;
   int32_t n = 0;
-  for (int g = tid; g < G; g += kThreads) {
+  for (int g = tid; g < G; g += kFinThreads) {
     z += (double)w.z[g];
     n += w.n[g];
   }
@@ -293,7 +343,7 @@ __global__ void __launch_bounds__(kThreads) router_finish(LossWs w, int G, int E
   zs[tid] = z;
   ns[tid] = n;
   __syncthreads();
-  for (int s = kThreads / 2; s > 0; s >>= 1) {
+  for (int s = kFinThreads / 2; s > 0; s >>= 1) {
     if (tid < s) {
       zs[tid] += zs[tid + s];
       ns[tid] += ns[tid + s];
@@ -314,6 +364,23 @@ __global__ void __launch_bounds__(kThreads) router_finish(LossWs w, int G, int E
 // ---------------------------------------------------------------------------
 // gradient of the logits
 // ---------------------------------------------------------------------------
+// The routing weights' part of a token, per pair j: dq_j = dw_j, or (dw_j - D) / S with
+// renormalised weights (S = sum q, D = sum q dw / S), and off = sum_j q_j dq_j over all pairs
+// (which is 0 with renormalised weights).
+//
+// More than 128 experts (a wave per token): lane j holds pair j.  Its q comes from its own
+// load of the logit (in cache by then), the sums over pairs are moves within 16 lanes, and
+// dq reaches the lanes that hold the experts through a zeroed row of LDS; pairs of the same
+// expert are first added in the order of j, so that each of them writes the same total.
+// Comparing each pair with each expert instead took 12 k NV vector instructions a lane
+// (131072 x 256, k = 8: 91 us so, @G@ us through LDS).  Fewer experts (several tokens per
+// wave) have few lanes per token and compare.
+template <int NV>
+struct Selected {
+  f32x4 a[NV];  // sum of dq over a lane's experts' pairs
+  float off;
+};
+
 template <int L, int NV, bool VEC>
 __global__ void __launch_bounds__(kThreads) router_grad(const float *__restrict__ logits,
                                                         const int32_t *__restrict__ idx,
@@ -322,8 +389,17 @@ __global__ void __launch_bounds__(kThreads) router_grad(const float *__restrict_
                                                         const float *__restrict__ dw, const float *__restrict__ dloss,
                                                         int64_t T, int E, int k, int renorm,
                                                         float *__restrict__ dlogits) {
-  constexpr int kGroups = kThreads / L;
-  const int tid = threadIdx.x, l = tid & (L - 1), grp = tid / L;
+  constexpr int kGroups = kThreads / L, kRow = L * 4 * NV;
+  constexpr bool kScatter = L == 64;
+  __shared__ __attribute__((aligned(16))) float rows[kScatter ? kGroups : 1][kScatter ? kRow : 1];
+  const int tid = threadIdx.x, l = tid & (L - 1);
+  const int grp = L == 64 ? __builtin_amdgcn_readfirstlane(tid >> 6) : tid / L;
+  float *row = rows[kScatter ? grp : 0];
+  if constexpr (kScatter) {
+#pragma unroll
+    for (int v = 0; v < 4 * NV; ++v) row[v * 64 + l] = 0.0f;  // this wave's own row: no barrier
+    wave_fence();
+  }
   // the losses' gradients per expert: g_b E f_e / n, and 2 g_z / n
   const int32_t n = counts[E];
   const float rn = n > 0 ? 1.0f / (float)n : 0.0f;
@@ -339,59 +415,111 @@ __global__ void __launch_bounds__(kThreads) router_grad(const float *__restrict_
     }
   for (int64_t t = (int64_t)blockIdx.x * kGroups + grp; t < T; t += (int64_t)gridDim.x * kGroups) {
     const bool use = !valid || valid[t];
+    const float *lrow = logits + t * E;
     f32x4 x[NV];
-    load_row<L, NV, VEC>(logits + t * E, E, l, use, x);
-    // A_e and, for renormalised weights, m_e
-    f32x4 a[NV] = {}, m[NV] = {};
-    if (dw && use)
-      for (int j = 0; j < k; ++j) {
-        const int i = idx[t * k + j];
-        const float d = dw[t * k + j];
+    load_row<L, NV, VEC>(lrow, E, l, use, x);
+    // pair l of the token (kScatter)
+    int pi = -1;
+    float pd = 0.0f, pl = -INFINITY;
+    if constexpr (kScatter) {
+      if (dw && use && l < k) {
+        pi = idx[t * k + l];
+        pd = dw[t * k + l];
+        if ((unsigned)pi < (unsigned)E)
+          pl = lrow[pi];
+        else
+          pi = -1;
+      }
+    }
+    float m, lse;
+    const float inv = softmax_row<L, NV>(x, lse, m);
+    Selected<NV> sel = {};
+    if constexpr (kScatter) {
+      if (dw) {
+        const float q = pi >= 0 ? exp_neg(pl - m) * inv : 0.0f;
+        pd = pi >= 0 ? pd : 0.0f;
+        float qd = q * pd, qs = q;
+        // over the first 16 lanes (the others hold none)
+        qd = group_sum<16>(qd);
+        qd = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(qd)));
+        if (renorm) {
+          qs = group_sum<16>(qs);
+          qs = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(qs)));
+          const float rs = qs > 0.0f ? 1.0f / qs : 0.0f;
+          pd = (pd - qd * rs) * rs;
+        } else {
+          sel.off = qd;
+        }
+        float sum = 0.0f;
+        for (int j = 0; j < k; ++j) {
+          const int ij = __builtin_amdgcn_readlane(pi, j);
+          const float dj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(pd), j));
+          sum += ij == pi ? dj : 0.0f;
+        }
+        // one wave's LDS operations complete in order: write, read by all lanes, clear
+        if (pi >= 0) row[VEC ? pi : slot_of<L, NV>(pi)] = sum;
+        wave_fence();
+#pragma unroll
+        for (int v = 0; v < NV; ++v) sel.a[v] = *reinterpret_cast<const f32x4 *>(row + 4 * (v * L + l));
+        wave_fence();
+        if (pi >= 0) row[VEC ? pi : slot_of<L, NV>(pi)] = 0.0f;
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v) x[v] *= inv;
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) x[v] *= inv;
+      if (dw && use) {
+        f32x4 mult[NV] = {};
+        for (int j = 0; j < k; ++j) {
+          const int i = idx[t * k + j];
+          const float d = dw[t * k + j];
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const bool hit = i == expert_of<L, NV, VEC>(v, c, l);
+              sel.a[v][c] += hit ? d : 0.0f;
+              mult[v][c] += hit ? 1.0f : 0.0f;
+            }
+        }
+        float sa = 0.0f, sm = 0.0f;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const bool hit = i == expert_of<L, NV, VEC>(v, c, l);
-            a[v][c] += hit ? d : 0.0f;
-            if (renorm) m[v][c] += hit ? 1.0f : 0.0f;
+            sa += x[v][c] * sel.a[v][c];
+            sm += x[v][c] * mult[v][c];
           }
-      }
-    float lse;
-    const float inv = softmax_row<L, NV>(x, lse);
-    float sf = 0.0f, sa = 0.0f, sm = 0.0f;
+        sa = group_sum<L>(sa);
+        if (renorm) {
+          sm = group_sum<L>(sm);
+          const float rs = sm > 0.0f ? 1.0f / sm : 0.0f, d = sa * rs;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      x[v] *= inv;
+          for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        sf += x[v][c] * fe[v][c];
-        sa += x[v][c] * a[v][c];
-        if (renorm) sm += x[v][c] * m[v][c];
+            for (int c = 0; c < 4; ++c) sel.a[v][c] = (sel.a[v][c] - d * mult[v][c]) * rs;
+        } else {
+          sel.off = sa;
+        }
       }
     }
+    float sf = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sf += x[v][c] * fe[v][c];
     sf = group_sum<L>(sf);
-    sa = group_sum<L>(sa);
-    float dm = 0.0f, rs = 1.0f, off = sa;  // routing weights: p (rs (A - dm m) - off)
-    if (renorm) {
-      sm = group_sum<L>(sm);
-      rs = sm > 0.0f ? 1.0f / sm : 0.0f;
-      dm = sa * rs;
-      off = 0.0f;
-    }
-    const float shift = gz * lse - sf - off;
+    const float shift = gz * lse - sf - sel.off;
     float *out = dlogits + t * E;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       f32x4 g;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float q = a[v][c];
-        if (renorm) q = (q - dm * m[v][c]) * rs;
-        g[c] = x[v][c] * (fe[v][c] + q + shift);
-      }
+      for (int c = 0; c < 4; ++c) g[c] = x[v][c] * (fe[v][c] + sel.a[v][c] + shift);
       if constexpr (VEC) {
         const int e = expert_of<L, NV, VEC>(v, 0, l);
-        if (e < E) *reinterpret_cast<f32x4 *>(out + e) = g;
+        if (e < E) __builtin_nontemporal_store(g, reinterpret_cast<f32x4 *>(out + e));
       } else {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -467,11 +595,11 @@ extern "C" bqm_status bqm_router_loss(const float *logits, const int32_t *topk_i
   const LossWs w = loss_ws(ws, g.G, E);
   hipStream_t s = as_stream(stream);
   with_shape(E, [&](auto L, auto NV, auto VEC) {
-    router_sums<L.value, NV.value, VEC.value><<<g.G, kThreads, 0, s>>>(logits, topk_idx, valid, T, E, k, w);
+    router_sums<L.value, NV.value, VEC.value><<<g.G, kSumThreads, kSumWaves * E * sizeof(float), s>>>(logits, topk_idx, valid, T, E, k, w);
   });
   st = launch_status("router_sums");
   if (st != BQM_OK) return st;
-  router_finish<<<(unsigned)cdiv(E, kFinE), kThreads, 0, s>>>(w, g.G, E, k, counts, loss);
+  router_finish<<<(unsigned)cdiv(E, kFinE), kFinThreads, 0, s>>>(w, g.G, E, k, counts, loss);
   return launch_status("router_finish");
 }
 

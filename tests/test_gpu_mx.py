@@ -635,3 +635,40 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     assert all(torch.equal(v, wa[n]) for n, v in a.outputs().items())
     assert all(torch.equal(v, wb[n]) for n, v in b.outputs().items())
+
+
+def test_binding_checks_every_tensor():
+    """Each argument of each call in turn with another type, layout or size (nothing is
+    launched: the checks come first)."""
+    import torch
+    log("binding checks")
+    bqm = _bqm()
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype, device=gpu())  # noqa: E731
+    f32, i32, u8 = torch.float32, torch.int32, torch.uint8
+    w, x = bqm.alloc_qtensor(bqm.FMT_MXFP4, 4, 64, 32), bqm.alloc_qtensor(bqm.FMT_MXFP4, 1, 8, 32)
+    calls = [
+        (bqm.bqm_mxfp4_gemm, [x, w, z(5, dtype=i32), z(8, dtype=i32), 1, z(8, 64)], (2, 3, 5)),
+        (bqm.bqm_mxfp4_dgrad, [w, z(8, 64), z(5, dtype=i32), z(8, dtype=i32), 1, z(8, 32)], (1, 2, 3, 5)),
+        (bqm.bqm_swiglu_ckpt_fwd, [z(4, 128), z(4, 128, dtype=u8), z(4, 4, dtype=u8), z(4, 64), None, z(1, dtype=i32)],
+         (0, 1, 2, 3, 5)),
+        (bqm.bqm_swiglu_ckpt_bwd, [z(4, 128, dtype=u8), z(4, 4, dtype=u8), z(4, 64), z(4, dtype=i32), z(4, dtype=f32),
+                                   z(4, 128), z(4, dtype=f32), z(1, dtype=i32)], (0, 1, 2, 3, 4, 5, 6, 7)),
+        (bqm.bqm_router_loss, [z(4, 8, dtype=f32), z(4, 2, dtype=i32), z(4, dtype=u8), z(9, dtype=i32), z(2, dtype=f32),
+                               z(1 << 16, dtype=u8)], (0, 1, 2, 3, 4)),
+        (bqm.bqm_router_grad, [z(4, 8, dtype=f32), z(4, 2, dtype=i32), z(4, dtype=u8), z(9, dtype=i32),
+                               z(4, 2, dtype=f32), z(2, dtype=f32), 0, z(4, 8, dtype=f32)], (0, 1, 2, 3, 4, 5, 7)),
+    ]
+    for f, args, tensors in calls:
+        f(*args)
+        for i in tensors:
+            t = args[i]
+            wide = torch.zeros(*t.shape, 2, dtype=t.dtype, device=t.device)[..., 0]
+            for other in (t.to(torch.float64), wide if t.numel() > 1 else None, t.cpu(),
+                          None if t is args[0] or t.numel() < 2 else t.reshape(-1)[1:].clone()):
+                if other is None:
+                    continue
+                if other.dim() < 2 <= t.dim() and f in (bqm.bqm_mxfp4_gemm, bqm.bqm_mxfp4_dgrad, bqm.bqm_swiglu_ckpt_bwd):
+                    other = t[1:].clone()
+                with pytest.raises((bqm.BQMError, ValueError, IndexError)):
+                    f(*args[:i], other, *args[i + 1:])
+    torch.cuda.synchronize()

@@ -109,25 +109,25 @@ def test_binding_checks_types_shapes_and_layout():
     z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)  # noqa: E731
     mxq = lambda n, r, c: bqm.alloc_qtensor(bqm.FMT_MXFP4, n, r, c, device="cpu")  # noqa: E731
     off, w, x = z(5, dtype=torch.int32), mxq(4, 64, 32), mxq(1, 8, 32)
+    f32, i32, u8 = torch.float32, torch.int32, torch.uint8
     bad = [
-        lambda: bqm.bqm_quantize_mxfp4(z(1, 8, 32, dtype=torch.float32), x),
-        lambda: bqm.bqm_quantize_mxfp4(z(1, 32, 8).transpose(1, 2), x),
-        lambda: bqm.bqm_quantize_mxfp4(z(1, 8, 64), x),
-        lambda: bqm.bqm_mxfp4_gemm(x, w, off[:4], None, 1, z(8, 64)),
-        lambda: bqm.bqm_mxfp4_gemm(x, w, off.long(), None, 1, z(8, 64)),
-        lambda: bqm.bqm_mxfp4_gemm(x, w, off, None, 1, z(8, 32)),
-        lambda: bqm.bqm_mxfp4_gemm(x, w, off, z(7, dtype=torch.int32), 1, z(8, 64)),
-        lambda: bqm.bqm_mxfp4_dgrad(w, z(8, 32), off, None, 1, z(8, 32)),
-        lambda: bqm.bqm_mxfp4_dgrad(w, z(64, 8).t(), off, None, 1, z(8, 32)),
-        lambda: bqm.bqm_swiglu_ckpt_fwd(z(4, 128), z(4, 64, dtype=torch.uint8), z(4, 4, dtype=torch.uint8)),
-        lambda: bqm.bqm_swiglu_ckpt_bwd(z(4, 128, dtype=torch.uint8), z(4, 4, dtype=torch.uint8), z(4, 64),
-                                        z(3, dtype=torch.int32), None, z(4, 128)),
-        lambda: bqm.bqm_router_loss(z(4, 8, dtype=torch.float32), z(4, 2, dtype=torch.int32), z(4, dtype=torch.bool),
-                                    z(9, dtype=torch.int32), z(2, dtype=torch.float32), None),
-        lambda: bqm.bqm_router_grad(z(4, 8), z(4, 2, dtype=torch.int32), None, z(9, dtype=torch.int32), None, None, 0,
-                                    z(4, 8, dtype=torch.float32)),
+        ("x: dtype", lambda: bqm.bqm_quantize_mxfp4(z(1, 8, 32, dtype=f32), x)),
+        ("x: not contiguous", lambda: bqm.bqm_quantize_mxfp4(z(1, 32, 8).transpose(1, 2), x)),
+        ("x: shape", lambda: bqm.bqm_quantize_mxfp4(z(1, 8, 64), x)),
+        ("x: not a GPU tensor", lambda: bqm.bqm_quantize_mxfp4(z(1, 8, 32), x)),
+        ("w: format", lambda: bqm.bqm_mxfp4_dgrad(bqm.alloc_qtensor(bqm.FMT_NF4, 4, 64, 64, device="cpu"), z(8, 64), off,
+                                                  None, 1, z(8, 64))),
+        ("not a GPU tensor", lambda: bqm.bqm_mxfp4_gemm(x, w, off, None, 1, z(8, 64))),
+        ("h: dtype", lambda: bqm.bqm_swiglu_ckpt_fwd(z(4, 128, dtype=f32), z(4, 128, dtype=u8), z(4, 4, dtype=u8))),
+        ("h: not contiguous", lambda: bqm.bqm_swiglu_ckpt_fwd(z(128, 4).t(), z(4, 128, dtype=u8), z(4, 4, dtype=u8))),
+        ("h8: shape", lambda: bqm.bqm_swiglu_ckpt_bwd(z(4, 64, dtype=u8), z(4, 4, dtype=u8), z(4, 64), None, None,
+                                                      z(4, 128))),
+        ("h8: dtype", lambda: bqm.bqm_swiglu_ckpt_bwd(z(4, 128), z(4, 4, dtype=u8), z(4, 64), None, None, z(4, 128))),
+        ("logits: dtype", lambda: bqm.bqm_router_grad(z(4, 8), z(4, 2, dtype=i32), None, z(9, dtype=i32), None, None, 0,
+                                                      z(4, 8, dtype=f32))),
+        ("logits: not contiguous", lambda: bqm.bqm_router_loss(z(8, 4, dtype=f32).t(), z(4, 2, dtype=i32), None,
+                                                               z(9, dtype=i32), z(2, dtype=f32), None)),
     ]
-    for i, f in enumerate(bad):
-        with pytest.raises(bqm.BQMError):
+    for what, f in bad:
+        with pytest.raises(bqm.BQMError, match=what):
             f()
-            pytest.fail(f"call {i} went through")
