@@ -62,8 +62,8 @@ __device__ __forceinline__ void dma_b128(const void *base, uint32_t off, uint32_
 __device__ __forceinline__ void dma_u8(const void *g, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, off" : : "v"(g), "s"(lds) : "memory", "m0");
 }
-__device__ __forceinline__ void dma_u8(const void *base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, %1"
+__device__ __forceinline__ void dma_b32(const void *base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
                :
                : "v"(off), "s"(base), "s"(lds)
                : "memory", "m0");
@@ -195,8 +195,8 @@ template <int TM, int TN, int NS>
 struct Smem<TM, TN, false, NS> {
   uint8_t a[NS][64 * TM * 128];
   uint16_t dq[2][TN][DK * DQS];
-  uint8_t c[NS][NTHR / 64][DK * 16 * (TN / 2)];  // each wave's codes of a step: 64 rows of its blocks
-  uint32_t cs[NS][NTHR / 64][TN / 2][DK];        // and their scales
+  uint8_t c[NS][DK * 128];          // codes of a step's weight rows, 256 columns
+  uint32_t cs[NS][2 * TN * DK];     // their scales: FAST [row][4 words, of which 2 hold bytes], else [block][row]
   int wsum[NTHR / 64], found[2];
 };
 
@@ -261,7 +261,8 @@ template <int TM, int TN, bool FWD, bool FAST, int NS>
 struct Tile {
   static constexpr int BM = 64 * TM, BN = 64 * TN;
   static constexpr int DB = TN / 2;  // dgrad: MX blocks a lane decodes per step
-  static constexpr int kCodeOps = FWD ? 0 : 2 * DB;  // dgrad: copies of codes and of scales per step
+  static constexpr int kCodeOps = FWD ? 0 : DB + (FAST ? 1 : DB);  // dgrad: copies of codes and scales per step
+  static_assert(FWD || TN == 4, "the gradient's code rows are 128 bytes");
   static constexpr bool DEEP = NS > 2;
   static constexpr int D = NS - 1;  // DEEP: steps the copies run ahead
   static_assert(!DEEP || !FWD, "the forward's scales are loaded one group ahead");
@@ -279,8 +280,8 @@ struct Tile {
   u32x4 va, vb;                 // their 16 bytes of the next group
   u32x4 cc[DB];                 // dgrad: codes of the next step
   uint32_t sc[DB];              // and their scales
-  int q0;                       // dgrad: first block of this wave
-  uint32_t coff[DB], soff[DB];  // dgrad, FAST: of codes and scales
+  int q0;                       // dgrad: first block of the tile's columns
+  uint32_t coff[DB], soff;      // dgrad, FAST: of codes and scales
   i32x4 af[2][TM], bf[2][TN];
   int ssa[TM], ssb[TN];         // forward: scale words of the step
   f32x16 acc[TM][TN];
@@ -328,13 +329,12 @@ struct Tile {
       sa = p.xs + src_row(p, (int64_t)rb + min(m0 + (tid < BM ? tid : 0), n_e - 1)) * nb;
     } else {
       sb = ws;
-      q0 = n0 / 32 + w * DB;
+      q0 = n0 / 32;
       if constexpr (FAST) {
 #pragma unroll
-        for (int i = 0; i < DB; ++i) {
-          coff[i] = (uint32_t)code_row(i) * (p.K / 2) + 16 * min(q0 + code_half(i), nb - 1);
-          soff[i] = (uint32_t)lane * nb + min(q0 + i, nb - 1);
-        }
+        for (int i = 0; i < DB; ++i)
+          coff[i] = (uint32_t)code_row(i) * (p.K / 2) + 16 * min(q0 + code_chunk(i), nb - 1);
+        soff = (uint32_t)(16 * w + (lane >> 2)) * nb + min(q0 + 4 * min(lane & 3, 1), nb - 4);
       }
     }
   }
@@ -391,41 +391,38 @@ struct Tile {
   __device__ __forceinline__ const uint32_t *scale_words(int ks) const { return sm.s[(ks >> 1) & 1][ks & 1][lane >> 5]; }
 
   // ---- dgrad: lane i of a wave decodes DB blocks of weight row i of the step ----
-  // The codes go to the wave's own LDS area two steps ahead (copies and not loads to
-  // registers: the compiler would wait for those without counting the copies in between).
-  // Row r keeps its half h of 32 bytes at h ^ (r >> 3 & 1) against bank conflicts.
-  __device__ __forceinline__ int code_row(int i) const { return (64 / DB) * i + lane / DB; }
-  __device__ __forceinline__ int code_half(int i) const {
-    return DB == 2 ? (lane & 1) ^ ((code_row(i) >> 3) & 1) : 0;
-  }
+  // The codes go through LDS, whole 128-byte rows like the activations', and are there one
+  // step before the activations of their step, as decoding comes first.  (Copies, not loads
+  // to registers: the compiler would wait for those without counting the copies in between.)
+  __device__ __forceinline__ int code_row(int i) const { return 8 * (DB * w + i) + (lane >> 3); }
+  __device__ __forceinline__ int code_chunk(int i) const { return (lane & 7) ^ ((code_row(i) >> 1) & 7); }
   __device__ __forceinline__ void code_op(int i, int ks) {
     const int d = ks & (NS - 1);
     if (i < DB) {
-      const uint32_t to = lds_addr(sm.c[d][w]) + 1024 * i;
+      const uint32_t to = lds_addr(sm.c[d]) + 1024 * (DB * w + i);
       if constexpr (FAST) {  // (past the last step: its rows again, which nothing reads)
         dma_b128(wbase + (int64_t)min(ks, nk - 1) * DK * (p.K / 2), coff[i], to);
       } else {
         const int64_t n = min(DK * ks + code_row(i), p.N - 1);  // past the end: the last row (its dY is zero)
-        const int q = min(q0 + code_half(i), nb - 1);           // past the end: columns that are dropped
+        const int q = min(q0 + code_chunk(i), nb - 1);          // past the end: columns that are dropped
         dma_b128(wbase + n * (p.K / 2) + 16 * q, to);
       }
+    } else if constexpr (FAST) {  // 16 rows a wave, 4 words each (the last two again the second)
+      dma_b32(sb + (int64_t)min(ks, nk - 1) * DK * nb, soff, lds_addr(sm.cs[d]) + 256 * w);
     } else {
-      const uint32_t to = lds_addr(sm.cs[d][w][i - DB]);
-      if constexpr (FAST) {
-        dma_u8(sb + (int64_t)min(ks, nk - 1) * DK * nb, soff[i - DB], to);
-      } else {
-        const int64_t n = min(DK * ks + lane, p.N - 1);
-        dma_u8(sb + n * nb + min(q0 + i - DB, nb - 1), to);
-      }
+      const int64_t n = min(DK * ks + lane, p.N - 1);
+      const int blk = w * DB + i - DB;
+      dma_u8(sb + n * nb + min(q0 + blk, nb - 1), lds_addr(sm.cs[d]) + 4 * DK * blk);
     }
   }
   __device__ __forceinline__ void read_codes(int ks) {
     const int d = ks & (NS - 1);
+    uint32_t two = 0;  // FAST: the scales of this lane's two blocks
+    if constexpr (FAST) two = reinterpret_cast<const uint16_t *>(sm.cs[d])[8 * lane + w];
 #pragma unroll
     for (int b = 0; b < DB; ++b) {
-      const int h = DB == 2 ? b ^ ((lane >> 3) & 1) : 0;
-      cc[b] = *reinterpret_cast<const u32x4 *>(sm.c[d][w] + 16 * (DB * lane + h));
-      sc[b] = sm.cs[d][w][b][lane];
+      cc[b] = *reinterpret_cast<const u32x4 *>(sm.c[d] + swz(lane, w * DB + b));
+      sc[b] = FAST ? (b ? two >> 8 : two & 0xFFu) : sm.cs[d][DK * (w * DB + b) + lane];
     }
   }
   // quarter u of the lane's blocks -> bf16 (exact) in buffer d
@@ -452,6 +449,16 @@ struct Tile {
       bf[k][tn] = frag_trans(sm.dq[st][c >> 6], 16 * kk, c & 63, lane);
   }
 
+  // the i-th of a slice's reads, in the order its MFMAs ask for them
+  __device__ __forceinline__ void read(int k, int i, int kk, int sa, int st) {
+    if (i == 0)
+      read_a(k, 0, kk, sa);
+    else if (i <= TN)
+      read_b(k, i - 1, kk, st);
+    else
+      read_a(k, i - TN, kk, sa);
+  }
+
   template <int KK>
   __device__ __forceinline__ void mfma(int k, int tm, int tn) {
     const i32x4 a = af[k][tm], b = bf[k][tn];
@@ -470,60 +477,42 @@ struct Tile {
   static constexpr int kCopies = 2 * TM + (FWD ? 2 * TN : 0), kFirst = DEEP ? 0 : kCopies / 2;
   static constexpr int kOps = kCopies + kCodeOps;  // per step
 
-  // Copies of this wave that its wait in slice 3 may leave in flight: those for later steps
-  // than the next
-  template <int LEFT>
-  static constexpr int in_flight() {
-    return DEEP ? (D - 1) * kOps : (LEFT > 1 ? kCodeOps : 0);
-  }
+  // Copies of this wave that its wait in slice 3 may leave in flight: those of later steps
+  static constexpr int kInFlight = DEEP ? (D - 1) * kOps : 0;
 
   // other work of slices 0-2, item i: fragment reads of the next slice, then copies and what
-  // becomes of them.  Slice 0: the rest of the next step's copies; forward: the scales of
-  // the next group (even steps); dgrad: the codes of the step after the next.  Slice 1:
-  // dgrad: the next step's codes are read and half decoded.  Slice 2: scales written, or the
-  // rest decoded.
+  // becomes of them.  Slice 0: the rest of the next step's copies (DEEP: all of step ks + D's,
+  // whose stage was read in step ks - 1, and the codes of the step after it), and the
+  // forward's scales of the next group (even steps).  Slice 1: dgrad: the next step's codes
+  // are read and half decoded.  Slice 2: scales written, or the rest decoded.
   template <int VT, int KK, int LEFT, int PAR>
   static constexpr int items() {
     const int reads = TN + VT;
     if (LEFT == 0) return reads;
-    if (KK == 0) return reads + (kCopies - kFirst) + (FWD ? (PAR == 0 ? 1 : 0) : (DEEP || LEFT > 1 ? kCodeOps : 0));
+    if (KK == 0) return reads + (kCopies - kFirst) + (FWD ? (PAR == 0 ? 1 : 0) : (DEEP ? kCodeOps : 0));
     if (KK == 1) return reads + (FWD ? 0 : 1 + 2 * DB);
     return reads + (FWD ? 1 : 2 * DB);
   }
   template <int VT, int KK, int LEFT, int PAR>
   __device__ __forceinline__ void item(int i, int ks, int st) {
     constexpr int k = (KK + 1) & 1;
-    if (i < TN) return read_b(k, i, KK + 1, st);
-    i -= TN;
-    if (i < VT) return read_a(k, i, KK + 1, stage(ks, st));
-    i -= VT;
+    if (i < TN + VT) return read(k, i, KK + 1, stage(ks, st), st);
+    i -= TN + VT;
     if constexpr (LEFT > 0) {
       if constexpr (KK == 0) {
-        // (DEEP: stage ks + D was read in step ks - 1)
         constexpr int ahead = DEEP ? D : 1;
         if (i < kCopies - kFirst) return copy(kFirst + i, ks + ahead, stage(ks + ahead, st ^ 1));
         i -= kCopies - kFirst;
-        if constexpr (FWD) {
-          // the next group, or the last again (it is then not used)
-          get_scales(min((ks >> 1) + 1, (nb - 1) >> 4));
-        } else {
-          code_op(i, ks + (DEEP ? D : 2));
-        }
+        if constexpr (FWD)
+          get_scales(min((ks >> 1) + 1, (nb - 1) >> 4));  // the last group again: it is then not used
+        else
+          code_op(i, ks + D + 1);
       } else if constexpr (KK == 1) {
         if constexpr (!FWD) {
-          if (i == 0) {
-            // this wave's codes of the next step, older than the copies of the step after
-            // it (the first kFirst) and than what slice 0 issued
-            if constexpr (DEEP)
-              wait_vm<(D - 1) * kOps>();
-            else if constexpr (LEFT > 1)
-              wait_vm<kCopies + kCodeOps>();
-            else
-              wait_vm<kCopies - kFirst>();
+          if (i == 0)
             read_codes(ks + 1);
-          } else {
+          else
             decode(i - 1, st ^ 1);
-          }
         }
       } else {
         if constexpr (FWD) {
@@ -551,7 +540,8 @@ struct Tile {
   // and the copies of the step after it begin
   template <int VT, int LEFT>
   __device__ __forceinline__ void slice3(int ks, int st) {
-    constexpr int NP = VT * TN, NR = TN + VT, NW = FWD ? NR : 0, NI = NR + NW + (LEFT > 1 && !DEEP ? kFirst : 0);
+    constexpr int NP = VT * TN, NR = TN + VT, NW = FWD ? NR : 0;
+    constexpr int NC = LEFT > 1 && !DEEP ? kCodeOps + kFirst : 0, NI = NR + NW + NC;
     int na[TM], nw[TN];
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
@@ -560,7 +550,7 @@ struct Tile {
         if (q == 0) {
           // every wave is done reading stage st, and the next stage is whole
           MX_PIN();
-          wait_vm<in_flight<LEFT>()>();
+          wait_vm<kInFlight>();
           barrier_lds();
           MX_PIN();
         }
@@ -568,18 +558,18 @@ struct Tile {
         if constexpr (FWD) sw = scale_words(ks + 1);
 #pragma unroll
         for (int i = q * NI / NP; i < (q + 1) * NI / NP; ++i) {
-          if (i < TN)
-            read_b(0, i, 0, st ^ 1);
-          else if (i < NR)
-            read_a(0, i - TN, 0, stage(ks + 1, st ^ 1));
-          else if (i < NR + NW) {
+          if (i < NR) {
+            read(0, i, 0, stage(ks + 1, st ^ 1), st ^ 1);
+          } else if (i < NR + NW) {
             const int j = i - NR;
             if (j < TN)
               nw[j] = (int)sw[BM + 32 * (wn * TN + j) + (lane & 31)];
             else
               na[j - TN] = (int)sw[32 * (2 * (j - TN) + wm) + (lane & 31)];
-          } else {
+          } else if (i < NR + NW + kFirst) {
             copy(i - NR - NW, ks + 2, st);
+          } else {
+            if constexpr (!FWD) code_op(i - NR - NW - kFirst, ks + 3);  // their place was read in slice 1
           }
         }
       }
@@ -618,36 +608,34 @@ struct Tile {
         vb = load_few_scales(sb, nb);
       }
     }
+    if constexpr (!FWD) {
+#pragma unroll
+      for (int i = 0; i < kCodeOps; ++i) code_op(i, 0);
+    }
 #pragma unroll
     for (int q = 0; q < (DEEP ? D : 1); ++q) {
       if constexpr (!FWD) {
 #pragma unroll
-        for (int i = 0; i < kCodeOps; ++i) code_op(i, q);
+        for (int i = 0; i < kCodeOps; ++i) code_op(i, q + 1);
       }
 #pragma unroll
       for (int j = 0; j < kCopies; ++j) copy(j, q, q);
     }
-    if constexpr (FWD) {
-      put_scales(0);
-    } else {
-      if constexpr (DEEP)
-        wait_vm<(D - 1) * kOps>();  // step 0's
-      else
-        wait_vm<kCopies>();  // this wave's codes
+    if constexpr (FWD) put_scales(0);
+    wait_vm<kInFlight>();
+    barrier_lds();
+    if constexpr (!FWD) {
       read_codes(0);
 #pragma unroll
       for (int u = 0; u < 4 * DB; ++u) decode(u, 0);
+      barrier_lds();
       if constexpr (!DEEP) {
 #pragma unroll
-        for (int i = 0; i < kCodeOps; ++i) code_op(i, 1);
+        for (int i = 0; i < kCodeOps; ++i) code_op(i, 2);
       }
     }
-    if constexpr (!DEEP) wait_vm<0>();
-    barrier_lds();
 #pragma unroll
-    for (int tn = 0; tn < TN; ++tn) read_b(0, tn, 0, 0);
-#pragma unroll
-    for (int tm = 0; tm < VT; ++tm) read_a(0, tm, 0, 0);
+    for (int i = 0; i < TN + VT; ++i) read(0, i, 0, 0, 0);
     if constexpr (FWD) {
       const uint32_t *sw = scale_words(0);
 #pragma unroll
@@ -670,7 +658,8 @@ struct Tile {
       ++ks;
     }
     step<VT, 0, -1>(ks, ks & 1);
-    if constexpr (DEEP) wait_vm<0>();  // the copies of no step, before the next tile's take their stages
+    // copies for steps that there are not, before the next tile's take their places
+    if (DEEP || (!FWD && nk == 1)) wait_vm<0>();
   }
 
   // rows: those of the tile that exist; ncols: columns of the output
@@ -806,7 +795,7 @@ constexpr int64_t kFewRows = 64, kManyRows = 128, kManyRowsDgrad = 96;
 template <bool FWD>
 bqm_status launch_tiles(MxParams p, hipStream_t s, const char *what) {
   const int64_t ncols = FWD ? p.N : p.K, alen = FWD ? p.K / 2 : 2 * (int64_t)p.N, most = (int64_t)1 << 32;
-  const bool fast = alen % 128 == 0 && (p.perm ? p.xrows : 256) * alen < most && (int64_t)p.N * (p.K / 2) < most;
+  const bool fast = alen % 128 == 0 && (FWD || p.K % 128 == 0) && (p.perm ? p.xrows : 256) * alen < most && (int64_t)p.N * (p.K / 2) < most;
   auto go = [&](auto TM, auto TN, auto OCC, auto NS) {
     constexpr int BM = 64 * TM.value, BN = 64 * TN.value;
     p.NT = (int)cdiv(ncols, BN);
