@@ -156,9 +156,9 @@ __device__ __forceinline__ int64_t src_row(const MxParams &p, int64_t pos) {
 // ---------------------------------------------------------------------------
 // the tiled kernels
 // ---------------------------------------------------------------------------
-// A workgroup of four waves (2 x 2) computes BM = 64 TM rows by BN = 64 TN columns of one
-// expert; wave (wm, wn) owns the 32-row tiles 2 tm + wm (interleaved, so that a partly
-// filled tile leaves both row halves the same work) of 32 TN columns.  The contraction goes
+// A workgroup of four waves (WM x WN) computes BM = 32 WM TM rows by BN = 32 WN TN columns of
+// one expert; wave (wm, wn) owns the 32-row tiles WM tm + wm (interleaved, so that a partly
+// filled tile leaves all rows of waves the same work) of 32 TN columns.  The contraction goes
 // in steps of 128 bytes per activation row (256 MXFP4 values or 64 bf16 values) through two
 // LDS stages filled by direct-to-LDS copies one step ahead; a step is four slices of
 // VT x TN MFMAs of 32x32.
@@ -182,21 +182,21 @@ __device__ __forceinline__ int64_t src_row(const MxParams &p, int64_t pos) {
 constexpr int DK = 64;   // dgrad: weight rows per step
 constexpr int DQS = 72;  // dgrad: row stride (bf16) of a decoded 64-column group
 
-template <int TM, int TN, bool FWD, int NS>
+template <int BM, int BN, bool FWD, int NS>
 struct Smem;
-template <int TM, int TN>
-struct Smem<TM, TN, true, 2> {
-  uint8_t a[2][64 * TM * 128];
-  uint8_t b[2][64 * TN * 128];
-  uint32_t s[2][2][2][64 * (TM + TN) + 4];  // [group parity][step of the group][half][row]
+template <int BM, int BN>
+struct Smem<BM, BN, true, 2> {
+  uint8_t a[2][BM * 128];
+  uint8_t b[2][BN * 128];
+  uint32_t s[2][2][2][BM + BN + 4];  // [group parity][step of the group][half][row]
   int wsum[NTHR / 64], found[2];
 };
-template <int TM, int TN, int NS>
-struct Smem<TM, TN, false, NS> {
-  uint8_t a[NS][64 * TM * 128];
-  uint16_t dq[2][TN][DK * DQS];
-  uint8_t c[NS][DK * 128];          // codes of a step's weight rows, 256 columns
-  uint32_t cs[NS][2 * TN * DK];     // their scales: FAST [row][4 words, of which 2 hold bytes], else [block][row]
+template <int BM, int BN, int NS>
+struct Smem<BM, BN, false, NS> {
+  uint8_t a[NS][BM * 128];
+  uint16_t dq[2][BN / 64][DK * DQS];
+  uint8_t c[NS][DK * 128];           // codes of a step's weight rows, 256 columns
+  uint32_t cs[NS][BN / 32 * DK];     // their scales: FAST [row][4 words, of which 2 hold bytes], else [block][row]
   int wsum[NTHR / 64], found[2];
 };
 
@@ -257,25 +257,26 @@ __device__ __forceinline__ float e8m0(uint32_t c) {
 // NS: stages.  Two: the copies of a step begin in slice 3 of the step before the last.  Four
 // (the gradient with few rows, where the activation stages are small): they run three steps
 // ahead, which a stream of weights from HBM needs when a step holds little else.
-template <int TM, int TN, bool FWD, bool FAST, int NS>
+template <int WM, int TM, int TN, bool FWD, bool FAST, int NS>
 struct Tile {
-  static constexpr int BM = 64 * TM, BN = 64 * TN;
-  static constexpr int DB = TN / 2;  // dgrad: MX blocks a lane decodes per step
+  static constexpr int WN = 4 / WM, BM = 32 * WM * TM, BN = 32 * WN * TN;
+  static constexpr int CA = BM / 32, CB = BN / 32;  // copies (of 8 rows) per wave and step
+  static constexpr int DB = BN / 128;  // dgrad: MX blocks a lane decodes per step
   static constexpr int kCodeOps = FWD ? 0 : DB + (FAST ? 1 : DB);  // dgrad: copies of codes and scales per step
-  static_assert(FWD || TN == 4, "the gradient's code rows are 128 bytes");
+  static_assert(FWD || BN == 256, "the gradient's code rows are 128 bytes");
   static constexpr bool DEEP = NS > 2;
   static constexpr int D = NS - 1;  // DEEP: steps the copies run ahead
   static_assert(!DEEP || !FWD, "the forward's scales are loaded one group ahead");
   const MxParams &p;
-  Smem<TM, TN, FWD, NS> &sm;
+  Smem<BM, BN, FWD, NS> &sm;
   int lane, w, wm, wn, nb, nk;
-  const uint8_t *asrc[FAST ? 1 : 2 * TM];  // activation rows of this lane's copies (bytes)
+  const uint8_t *asrc[FAST ? 1 : CA];  // activation rows of this lane's copies (bytes)
   const uint8_t *abase;                    // FAST: what aoff counts from
-  uint32_t aoff[FAST ? 2 * TM : 1];
+  uint32_t aoff[FAST ? CA : 1];
   int alen;                     // bytes of an activation row
   const uint8_t *zeros;
   const uint8_t *wbase;         // the expert's codes
-  uint32_t boff[FWD ? 2 * TN : 1];
+  uint32_t boff[FWD ? CB : 1];
   const uint8_t *sa, *sb;       // forward: the scale rows this thread carries
   u32x4 va, vb;                 // their 16 bytes of the next group
   u32x4 cc[DB];                 // dgrad: codes of the next step
@@ -286,11 +287,11 @@ struct Tile {
   int ssa[TM], ssb[TN];         // forward: scale words of the step
   f32x16 acc[TM][TN];
 
-  __device__ __forceinline__ Tile(const MxParams &p_, Smem<TM, TN, FWD, NS> &sm_) : p(p_), sm(sm_) {
+  __device__ __forceinline__ Tile(const MxParams &p_, Smem<BM, BN, FWD, NS> &sm_) : p(p_), sm(sm_) {
     lane = threadIdx.x & 63;
     w = wave_id();
-    wm = w >> 1;
-    wn = w & 1;
+    wm = WM == 2 ? w >> 1 : 0;
+    wn = WM == 2 ? w & 1 : w;
     nb = p.K / 32;
     nk = FWD ? (p.K + 255) / 256 : (p.N + DK - 1) / DK;
     alen = FWD ? p.K / 2 : p.N * 2;
@@ -304,8 +305,8 @@ struct Tile {
     // spilled, and the wait for its reload lands inside the K loop
     asm volatile("" : "+v"(lane));
 #pragma unroll
-    for (int j = 0; j < 2 * TM; ++j) {
-      const int r = 8 * (2 * TM * w + j) + (lane >> 3);
+    for (int j = 0; j < CA; ++j) {
+      const int r = 8 * (CA * w + j) + (lane >> 3);
       const uint8_t *x = FWD ? p.xc : reinterpret_cast<const uint8_t *>(p.dy);
       const int64_t row = src_row(p, (int64_t)rb + min(m0 + r, n_e - 1));
       if constexpr (FAST) {
@@ -321,8 +322,8 @@ struct Tile {
     const uint8_t *ws = p.ws + (int64_t)e * p.N * nb;
     if constexpr (FWD) {
 #pragma unroll
-      for (int j = 0; j < 2 * TN; ++j) {
-        const int r = 8 * (2 * TN * w + j) + (lane >> 3);
+      for (int j = 0; j < CB; ++j) {
+        const int r = 8 * (CB * w + j) + (lane >> 3);
         boff[j] = (uint32_t)min(n0 + r, p.N - 1) * (p.K / 2) + (FAST ? 16 * ((lane & 7) ^ ((r >> 1) & 7)) : 0);
       }
       sb = ws + (int64_t)min(n0 + (tid < BN ? tid : 0), p.N - 1) * nb;
@@ -342,23 +343,23 @@ struct Tile {
   // copy j of step ks into stage st: activations (j < 2 TM; zeros past the row's end), then
   // weights (any of the row's bytes there)
   __device__ __forceinline__ void copy(int j, int ks, int st) {
-    if (j < 2 * TM) {
-      const uint32_t to = lds_addr(sm.a[st]) + 1024 * (2 * TM * w + j);
+    if (j < CA) {
+      const uint32_t to = lds_addr(sm.a[st]) + 1024 * (CA * w + j);
       if constexpr (FAST) {
         // (DEEP: past the last step its bytes again, which nothing reads)
         dma_b128(abase + 128 * (DEEP ? min(ks, nk - 1) : ks), aoff[j], to);
       } else {
-        const int r = 8 * (2 * TM * w + j) + (lane >> 3);
+        const int r = 8 * (CA * w + j) + (lane >> 3);
         const int o = 128 * ks + 16 * ((lane & 7) ^ ((r >> 1) & 7));
         dma_b128(o < alen ? asrc[j] + o : zeros, to);
       }
     } else if constexpr (FWD) {
-      j -= 2 * TM;
-      const uint32_t to = lds_addr(sm.b[st]) + 1024 * (2 * TN * w + j);
+      j -= CA;
+      const uint32_t to = lds_addr(sm.b[st]) + 1024 * (CB * w + j);
       if constexpr (FAST) {
         dma_b128(wbase + 128 * ks, boff[j], to);
       } else {
-        const int r = 8 * (2 * TN * w + j) + (lane >> 3);
+        const int r = 8 * (CB * w + j) + (lane >> 3);
         const int o = 128 * ks + 16 * ((lane & 7) ^ ((r >> 1) & 7));
         dma_b128(wbase + (boff[j] + (uint32_t)(o < alen ? o : 0)), to);
       }
@@ -376,7 +377,7 @@ struct Tile {
   __device__ __forceinline__ void put_words(const u32x4 &v, int group, int row) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t(&s)[2][64 * (TM + TN) + 4] = sm.s[group & 1][h];
+      uint32_t(&s)[2][BM + BN + 4] = sm.s[group & 1][h];
       s[0][row] = __builtin_amdgcn_perm(v[2 * h + 1], v[2 * h], 0x06040200u);
       s[1][row] = __builtin_amdgcn_perm(v[2 * h + 1], v[2 * h], 0x07050301u);
     }
@@ -439,7 +440,7 @@ struct Tile {
 
   // ---- fragments of slice kk of stage st into set k ----
   __device__ __forceinline__ void read_a(int k, int tm, int kk, int st) {
-    af[k][tm] = *reinterpret_cast<const i32x4 *>(sm.a[st] + swz(32 * (2 * tm + wm) + (lane & 31), 2 * kk + (lane >> 5)));
+    af[k][tm] = *reinterpret_cast<const i32x4 *>(sm.a[st] + swz(32 * (WM * tm + wm) + (lane & 31), 2 * kk + (lane >> 5)));
   }
   __device__ __forceinline__ void read_b(int k, int tn, int kk, int st) {
     const int c = 32 * (wn * TN + tn);
@@ -474,7 +475,7 @@ struct Tile {
   // The copies of step ks + 2 go into the stage that step ks has finished reading: the first
   // half from slice 3 of step ks on (after its barrier), the rest in slice 0 of step ks + 1.
   // LEFT: steps that follow (0, 1, or 2 for more).  PAR: the step's parity (-1: not known).
-  static constexpr int kCopies = 2 * TM + (FWD ? 2 * TN : 0), kFirst = DEEP ? 0 : kCopies / 2;
+  static constexpr int kCopies = CA + (FWD ? CB : 0), kFirst = DEEP ? 0 : kCopies / 2;
   static constexpr int kOps = kCopies + kCodeOps;  // per step
 
   // Copies of this wave that its wait in slice 3 may leave in flight: those of later steps
@@ -565,7 +566,7 @@ struct Tile {
             if (j < TN)
               nw[j] = (int)sw[BM + 32 * (wn * TN + j) + (lane & 31)];
             else
-              na[j - TN] = (int)sw[32 * (2 * (j - TN) + wm) + (lane & 31)];
+              na[j - TN] = (int)sw[32 * (WM * (j - TN) + wm) + (lane & 31)];
           } else if (i < NR + NW + kFirst) {
             copy(i - NR - NW, ks + 2, st);
           } else {
@@ -641,7 +642,7 @@ struct Tile {
 #pragma unroll
       for (int tn = 0; tn < TN; ++tn) ssb[tn] = (int)sw[BM + 32 * (wn * TN + tn) + (lane & 31)];
 #pragma unroll
-      for (int tm = 0; tm < VT; ++tm) ssa[tm] = (int)sw[32 * (2 * tm + wm) + (lane & 31)];
+      for (int tm = 0; tm < VT; ++tm) ssa[tm] = (int)sw[32 * (WM * tm + wm) + (lane & 31)];
     }
     if (!DEEP && nk > 1) {
 #pragma unroll
@@ -667,7 +668,7 @@ struct Tile {
   __device__ __forceinline__ void store(int64_t row_base, int rows, int n0, int ncols) {
 #pragma unroll
     for (int tm = 0; tm < VT; ++tm) {
-      const int r = 32 * (2 * tm + wm) + (lane & 31);
+      const int r = 32 * (WM * tm + wm) + (lane & 31);
       if (r < rows) {
         uint16_t *o = p.out + (row_base + r) * ncols;
 #pragma unroll
@@ -690,10 +691,11 @@ struct Tile {
   }
 };
 
-template <int TM, int TN, bool FWD, bool FAST, int OCC, int NS>
+template <int WM, int TM, int TN, bool FWD, bool FAST, int OCC, int NS>
 __global__ void __launch_bounds__(NTHR, OCC) mx_tiles(MxParams p) {
-  __shared__ __attribute__((aligned(16))) Smem<TM, TN, FWD, NS> sm;
-  constexpr int BM = 64 * TM, BN = 64 * TN;
+  using T = Tile<WM, TM, TN, FWD, FAST, NS>;
+  constexpr int BM = T::BM, BN = T::BN;
+  __shared__ __attribute__((aligned(16))) Smem<BM, BN, FWD, NS> sm;
   const int ncols = FWD ? p.N : p.K;
   TileMap map;
   const int total = map.build<BM>(p, sm.wsum) * p.NT;
@@ -701,7 +703,7 @@ __global__ void __launch_bounds__(NTHR, OCC) mx_tiles(MxParams p) {
   // flight there share an expert's rows and weights in its L2
   const int per = (total + 7) / 8;
   const int first = (blockIdx.x & 7) * per, last = min(first + per, total);
-  Tile<TM, TN, FWD, FAST, NS> t(p, sm);
+  T t(p, sm);
   for (int L = first + (int)(blockIdx.x >> 3); L < last; L += (int)(gridDim.x >> 3)) {
     const int mt = L / p.NT, n0 = (L % p.NT) * BN;
     map.find(mt, sm.found);
@@ -710,7 +712,7 @@ __global__ void __launch_bounds__(NTHR, OCC) mx_tiles(MxParams p) {
     const int rb = seg_at(p, e), n_e = seg_at(p, e + 1) - rb;
     const int m0 = (mt - __builtin_amdgcn_readfirstlane(sm.found[1])) * BM;
     const int rows = min(n_e - m0, BM);
-    const int vt = (rows + 63) / 64;  // row tiles per wave that hold rows
+    const int vt = (rows + 32 * WM - 1) / (32 * WM);  // row tiles per wave that hold rows
     t.setup(e, rb, m0, n_e, n0);
     const int64_t row_base = (int64_t)rb + m0;
     if constexpr (TM == 1) {
@@ -785,39 +787,59 @@ bqm_status check_routed(const char *who, const bqm_qtensor *w, const int32_t *of
 
 constexpr int kCUs = 256;
 
-// Tile size by the rows an expert has on average (the host knows R and E, not the offsets).
-// Measured with N = 2816 (gradient: 2048) and K = 2048 over 60 (64) experts, us at 16, 64,
-// 100, 160 and 256 rows (gradient: 12, 64, 128 and 256) an expert:
-//   product   64 x 128: 44 54 68 91 119    128 x 128: 46 55 63 83 97    256 x 256: 54 61 68 77 94
-//   gradient  64 x 256: @DG@               256 x 256: 72 74 88 132
-constexpr int64_t kFewRows = 64, kManyRows = 128, kManyRowsDgrad = 96;
+// The tile goes by the rows an expert has on average (the host knows R and E, not the
+// offsets), one tile of rows as long as it can hold them: every further one reads the
+// expert's weights again, and a tile's empty rows cost what full ones do.  Measured at
+// N = 2816, K = 2048, 60 experts (gradient N = 2048, 64 experts), us at the given rows:
+//   product   rows  1   16   32   60  100  160  256   gradient  rows 12   32   64  100  256
+//   32 x 128       41   43   47   60                  32 x 256       48   49   96   90
+//   64 x 128       42   45   48   54   68   91  119   64 x 256       56   58   64   95  227
+//   128 x 128      43   46   50   55   63   83   97
+//   256 x 256      52   54   56   61   68   77   94   256 x 256      72   72   74   81  132
+// Contractions that are not whole steps (FAST false) have the middle and the largest tile.
+constexpr int64_t kRows32 = 24, kRows64 = 64, kRows128 = 128, kRowsDgrad64 = 88;
 
 template <bool FWD>
 bqm_status launch_tiles(MxParams p, hipStream_t s, const char *what) {
   const int64_t ncols = FWD ? p.N : p.K, alen = FWD ? p.K / 2 : 2 * (int64_t)p.N, most = (int64_t)1 << 32;
-  const bool fast = alen % 128 == 0 && (FWD || p.K % 128 == 0) && (p.perm ? p.xrows : 256) * alen < most && (int64_t)p.N * (p.K / 2) < most;
-  auto go = [&](auto TM, auto TN, auto OCC, auto NS) {
-    constexpr int BM = 64 * TM.value, BN = 64 * TN.value;
+  const bool fast = alen % 128 == 0 && (FWD || p.K % 128 == 0) && (p.perm ? p.xrows : 256) * alen < most &&
+                    (int64_t)p.N * (p.K / 2) < most;
+  auto go = [&](auto WM, auto TM, auto TN, auto FAST, auto OCC, auto NS) {
+    constexpr int BM = 32 * WM.value * TM.value, BN = 32 * (4 / WM.value) * TN.value;
     p.NT = (int)cdiv(ncols, BN);
     // at most R / BM + E row tiles; as many workgroups as the chip holds at once
     const int64_t tiles = (p.R / BM + (p.E < p.R ? p.E : p.R)) * p.NT, slots = (int64_t)kCUs * OCC.value;
     const unsigned grid = (unsigned)(cdiv(tiles < slots ? tiles : slots, 8) * 8);
-    if (fast)
-      mx_tiles<TM.value, TN.value, FWD, true, OCC.value, NS.value><<<grid, NTHR, 0, s>>>(p);
-    else
-      mx_tiles<TM.value, TN.value, FWD, false, OCC.value, NS.value><<<grid, NTHR, 0, s>>>(p);
+    mx_tiles<WM.value, TM.value, TN.value, FWD, FAST.value, OCC.value, NS.value><<<grid, NTHR, 0, s>>>(p);
   };
   constexpr std::integral_constant<int, 1> one;
   constexpr std::integral_constant<int, 2> two;
+  constexpr std::integral_constant<int, 3> three;
   constexpr std::integral_constant<int, 4> four;
-  if (p.R >= (FWD ? kManyRows : kManyRowsDgrad) * p.E)
-    go(four, four, one, two);
-  else if constexpr (!FWD)
-    go(one, four, one, four);
-  else if (p.R >= kFewRows * p.E)
-    go(two, two, two, two);
-  else
-    go(one, two, two, two);
+  constexpr std::true_type yes;
+  constexpr std::false_type no;
+  const int64_t E = p.E;
+  if constexpr (FWD) {
+    if (p.R >= kRows128 * E)
+      fast ? go(two, four, four, yes, one, two) : go(two, four, four, no, one, two);
+    else if (!fast)
+      go(two, two, two, no, two, two);
+    else if (p.R >= kRows64 * E)
+      go(two, two, two, yes, two, two);
+    else if (p.R >= kRows32 * E)
+      go(two, one, two, yes, two, two);
+    else
+      go(one, one, one, yes, three, two);
+  } else {
+    if (p.R >= kRowsDgrad64 * E)
+      fast ? go(two, four, four, yes, one, two) : go(two, four, four, no, one, two);
+    else if (!fast)
+      go(two, one, four, no, one, four);
+    else if (p.R >= kRows32 * E)
+      go(two, one, four, yes, one, four);
+    else
+      go(one, one, two, yes, one, four);
+  }
   return launch_status(what);
 }
 
