@@ -249,11 +249,13 @@ __device__ __forceinline__ float e8m0(uint32_t c) {
 }
 
 // Everything a wave keeps while it works on one tile.
-// FAST: the contraction is whole steps and every source lies within 4 GiB of a base, so a
-// copy's address is a scalar base that moves with the step plus the lane's constant offset.
-// Without it copies take 64-bit addresses, and zeros past the end of an activation row: four
-// to six more vector instructions for each (product of the training batch, 65536 x 4096 x
-// 6144: 1080 us so, 1072 us with FAST; gradient 2830 and 2755 us).
+// FAST: the contraction has at least one whole step and every source lies within 4 GiB of a
+// base, so a copy's address is a scalar base that moves with the step plus the lane's
+// constant offset.  Where the last step is not whole it takes the last 128 bytes of the rows
+// instead, and the fragments' share of the step before is replaced by zeros.  Without FAST
+// copies take 64-bit addresses, and zeros past the end of an activation row: four to six more
+// vector instructions for each (64 experts of 1024 rows, product 4096 x 6176: 1322 us so,
+// 1271 us with FAST; gradient 4128 x 6144: 2985 and 2778 us).
 // NS: stages.  Two: the copies of a step begin in slice 3 of the step before the last.  Four
 // (the gradient with few rows, where the activation stages are small): they run three steps
 // ahead, which a stream of weights from HBM needs when a step holds little else.
@@ -340,14 +342,20 @@ struct Tile {
     }
   }
 
+  // FAST: where step ks begins in its rows, and the dgrad's weight rows (steps past the last
+  // are the last again: copied for nothing, and not read)
+  __device__ __forceinline__ int at_step(int ks) const { return min(128 * ks, alen - 128); }
+  __device__ __forceinline__ int64_t row_at(int ks) const { return min(DK * ks, p.N - DK); }
+  // the last step's 16-byte chunks that belong to the step before
+  __device__ __forceinline__ int overlap() const { return FAST ? 8 * nk - alen / 16 : 0; }
+
   // copy j of step ks into stage st: activations (j < 2 TM; zeros past the row's end), then
   // weights (any of the row's bytes there)
   __device__ __forceinline__ void copy(int j, int ks, int st) {
     if (j < CA) {
       const uint32_t to = lds_addr(sm.a[st]) + 1024 * (CA * w + j);
       if constexpr (FAST) {
-        // (DEEP: past the last step its bytes again, which nothing reads)
-        dma_b128(abase + 128 * (DEEP ? min(ks, nk - 1) : ks), aoff[j], to);
+        dma_b128(abase + at_step(ks), aoff[j], to);
       } else {
         const int r = 8 * (CA * w + j) + (lane >> 3);
         const int o = 128 * ks + 16 * ((lane & 7) ^ ((r >> 1) & 7));
@@ -357,7 +365,7 @@ struct Tile {
       j -= CA;
       const uint32_t to = lds_addr(sm.b[st]) + 1024 * (CB * w + j);
       if constexpr (FAST) {
-        dma_b128(wbase + 128 * ks, boff[j], to);
+        dma_b128(wbase + at_step(ks), boff[j], to);
       } else {
         const int r = 8 * (CB * w + j) + (lane >> 3);
         const int o = 128 * ks + 16 * ((lane & 7) ^ ((r >> 1) & 7));
@@ -375,19 +383,23 @@ struct Tile {
   // for each step and half g of a wave: the scales of blocks g, 2 + g, 4 + g, 6 + g as one
   // word, of which the MFMA of slice kk takes byte kk
   __device__ __forceinline__ void put_words(const u32x4 &v, int group, int row) {
+    const u32x4 u = shift_scales(v, group, nb);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      // FAST: the last step's eight blocks are the row's last, the top half of what was loaded
+      const bool last = FAST && 2 * group + h == nk - 1;
+      const uint32_t lo = last ? v[2] : u[2 * h], hi = last ? v[3] : u[2 * h + 1];
       uint32_t(&s)[2][BM + BN + 4] = sm.s[group & 1][h];
-      s[0][row] = __builtin_amdgcn_perm(v[2 * h + 1], v[2 * h], 0x06040200u);
-      s[1][row] = __builtin_amdgcn_perm(v[2 * h + 1], v[2 * h], 0x07050301u);
+      s[0][row] = __builtin_amdgcn_perm(hi, lo, 0x06040200u);
+      s[1][row] = __builtin_amdgcn_perm(hi, lo, 0x07050301u);
     }
   }
   __device__ __forceinline__ void put_scales(int group) {
     // threads without a row write to a word past the rows': a branch here would let the
     // compiler move MFMAs past it, out of their order
     const int tid = threadIdx.x, none = BM + BN;
-    put_words(shift_scales(va, group, nb), group, BM == NTHR || tid < BM ? tid : none);
-    put_words(shift_scales(vb, group, nb), group, BN == NTHR || tid < BN ? BM + tid : none);
+    put_words(va, group, BM == NTHR || tid < BM ? tid : none);
+    put_words(vb, group, BN == NTHR || tid < BN ? BM + tid : none);
   }
   __device__ __forceinline__ const uint32_t *scale_words(int ks) const { return sm.s[(ks >> 1) & 1][ks & 1][lane >> 5]; }
 
@@ -401,15 +413,15 @@ struct Tile {
     const int d = ks & (NS - 1);
     if (i < DB) {
       const uint32_t to = lds_addr(sm.c[d]) + 1024 * (DB * w + i);
-      if constexpr (FAST) {  // (past the last step: its rows again, which nothing reads)
-        dma_b128(wbase + (int64_t)min(ks, nk - 1) * DK * (p.K / 2), coff[i], to);
+      if constexpr (FAST) {
+        dma_b128(wbase + row_at(ks) * (p.K / 2), coff[i], to);
       } else {
         const int64_t n = min(DK * ks + code_row(i), p.N - 1);  // past the end: the last row (its dY is zero)
         const int q = min(q0 + code_chunk(i), nb - 1);          // past the end: columns that are dropped
         dma_b128(wbase + n * (p.K / 2) + 16 * q, to);
       }
     } else if constexpr (FAST) {  // 16 rows a wave, 4 words each (the last two again the second)
-      dma_b32(sb + (int64_t)min(ks, nk - 1) * DK * nb, soff, lds_addr(sm.cs[d]) + 256 * w);
+      dma_b32(sb + row_at(ks) * nb, soff, lds_addr(sm.cs[d]) + 256 * w);
     } else {
       const int64_t n = min(DK * ks + lane, p.N - 1);
       const int blk = w * DB + i - DB;
@@ -525,8 +537,19 @@ struct Tile {
     }
   }
 
+  // zeros in place of the activations of slice kk of the last step that the step before had
+  template <int VT>
+  __device__ __forceinline__ void drop_overlap(int kk) {
+    const bool drop = 2 * kk + (lane >> 5) < overlap();
+#pragma unroll
+    for (int tm = 0; tm < VT; ++tm)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) af[kk & 1][tm][i] = drop ? 0 : af[kk & 1][tm][i];
+  }
+
   template <int VT, int KK, int LEFT, int PAR>
   __device__ __forceinline__ void slice(int ks, int st) {
+    if constexpr (FAST && LEFT == 0) drop_overlap<VT>(KK);
     constexpr int NP = VT * TN, NI = items<VT, KK, LEFT, PAR>();
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
@@ -543,6 +566,7 @@ struct Tile {
   __device__ __forceinline__ void slice3(int ks, int st) {
     constexpr int NP = VT * TN, NR = TN + VT, NW = FWD ? NR : 0;
     constexpr int NC = LEFT > 1 && !DEEP ? kCodeOps + kFirst : 0, NI = NR + NW + NC;
+    if constexpr (FAST && LEFT == 0) drop_overlap<VT>(3);
     int na[TM], nw[TN];
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
@@ -796,13 +820,13 @@ constexpr int kCUs = 256;
 //   64 x 128       42   45   48   54   68   91  119   64 x 256       56   58   64   95  227
 //   128 x 128      43   46   50   55   63   83   97
 //   256 x 256      52   54   56   61   68   77   94   256 x 256      72   72   74   81  132
-// Contractions that are not whole steps (FAST false) have the middle and the largest tile.
+// Without FAST there are the middle and the largest tile.
 constexpr int64_t kRows32 = 24, kRows64 = 64, kRows128 = 128, kRowsDgrad64 = 88;
 
 template <bool FWD>
 bqm_status launch_tiles(MxParams p, hipStream_t s, const char *what) {
   const int64_t ncols = FWD ? p.N : p.K, alen = FWD ? p.K / 2 : 2 * (int64_t)p.N, most = (int64_t)1 << 32;
-  const bool fast = alen % 128 == 0 && (FWD || p.K % 128 == 0) && (p.perm ? p.xrows : 256) * alen < most &&
+  const bool fast = alen >= 128 && (FWD || p.K % 128 == 0) && (p.perm ? p.xrows : 256) * alen < most &&
                     (int64_t)p.N * (p.K / 2) < most;
   auto go = [&](auto WM, auto TM, auto TN, auto FAST, auto OCC, auto NS) {
     constexpr int BM = 32 * WM.value * TM.value, BN = 32 * (4 / WM.value) * TN.value;
