@@ -167,7 +167,7 @@ __device__ __forceinline__ f32x2 e4m3_pair(uint32_t w) {
   return __builtin_amdgcn_cvt_pk_f32_fp8((int)w, HI);
 }
 
-// L = 2^logL lanes per row (4 to 64): with few elements a wave takes 64 / L rows
+// L = 2^logL lanes per row (up to 64): with few elements a wave takes 64 / L rows
 __global__ void __launch_bounds__(kThreads) swiglu_ckpt_bwd(const uint8_t *__restrict__ h8,
                                                             const uint8_t *__restrict__ h8s,
                                                             const uint16_t *__restrict__ da,
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_ckpt_bwd(const uint8_t *__res
         const float s = sigmoid_f(g), gsg = g * s;
         dot += dv * gsg * u;
         const float wd = w * dv;
-        dgv[j] = wd * u * s * (1.0f + g * (1.0f - s));
+        dgv[j] = wd * (u * s) * (1.0f + g * (1.0f - s));
         duv[j] = wd * gsg;
       }
       dg[i] = pack_bf16_rne(dgv[0], dgv[1]);
@@ -279,6 +279,7 @@ extern "C" bqm_status bqm_swiglu_ckpt_bwd(const uint8_t *h8, const uint8_t *h8_s
   const uint32_t upr = (uint32_t)(I / 8);
   int logL = 2;
   while (logL < 6 && (1u << logL) < upr) ++logL;
+  while ((R << logL) >= (int64_t)1 << 32) --logL;  // a launch has less than 2^32 threads
   const int64_t grid = cdiv(R << logL, kThreads);
   swiglu_ckpt_bwd<<<(unsigned)grid, kThreads, 0, as_stream(stream)>>>(h8, h8_scales, da, perm, topk_w, R, upr, logL,
                                                                       n_rows, dh, dtopk_w);
