@@ -97,7 +97,7 @@ __device__ __forceinline__ int swz(int row, int c) { return row * 128 + 16 * (c 
 // ---------------------------------------------------------------------------
 // tiles
 // ---------------------------------------------------------------------------
-// First rows of the experts' segments, clamped to [0, R] and non-decreasing
+// first row of expert e's segment, clamped to [0, R]
 __device__ __forceinline__ int seg_at(const MxParams &p, int e) {
   const int64_t v = p.offsets[e];
   return (int)(v < 0 ? 0 : (v > p.R ? p.R : v));
@@ -813,7 +813,7 @@ bqm_status check_routed(const char *who, const bqm_qtensor *w, const int32_t *of
   BQM_REQUIRE(R < ((int64_t)1 << 30), BQM_ERR_SHAPE, "%s: R=%lld too large", who, (long long)R);
   if (perm) {
     BQM_REQUIRE(k >= 1, BQM_ERR_SHAPE, "%s: k=%d < 1", who, k);
-    BQM_REQUIRE(rows * k == R, BQM_ERR_SHAPE, "%s: R=%lld is not %lld rows times k=%d", who, (long long)R,
+    BQM_REQUIRE(rows <= R && rows * k == R, BQM_ERR_SHAPE, "%s: R=%lld is not %lld rows times k=%d", who, (long long)R,
                 (long long)rows, k);
   } else {
     BQM_REQUIRE(rows == R, BQM_ERR_SHAPE, "%s: R=%lld, but %lld rows and no perm", who, (long long)R, (long long)rows);

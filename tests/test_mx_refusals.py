@@ -51,6 +51,7 @@ def test_gemm(lib):
     assert f(R=63) == -2                               # rows without perm
     assert f(perm=16, k=2, R=127) == -2 and f(perm=16, k=0, R=64) == -2
     assert f(R=-1) == -1
+    assert f(x=q(rows=1 << 62), perm=16, k=4, R=0) == -2   # rows k = 0 in 64 bits
     assert f(off=None) == -1 and f(off=20) == -3 and f(perm=20) == -3
     assert f(y=None) == -1 and f(y=20) == -3
     assert f(x=q(codes=None)) == -1 and f(w=q(n=4, scales=18)) == -3
@@ -90,7 +91,7 @@ def test_router(lib):
     def f(l=16, idx=16, valid=None, T=4, E=8, k=2, counts=16, loss=16, ws=16, wsb=1 << 30):
         return lib.bqm_router_loss(l, idx, valid, T, E, k, counts, loss, ws, wsb, None)
     assert f(E=0) == -2 and f(E=1025) == -2 and f(k=9) == -2 and f(k=0) == -2 and f(E=64, k=17) == -2
-    assert f(T=-1) == -1 and f(T=1 << 30) == -2
+    assert f(T=-1) == -1 and f(T=1 << 30) == -2 and f(T=1 << 62, k=4) == -2   # T k = 0 in 64 bits
     assert f(l=None) == -1 and f(idx=None) == -1 and f(counts=None) == -1 and f(loss=None) == -1
     assert f(l=8) == -3 and f(valid=8) == -3 and f(loss=8) == -3 and f(ws=8) == -3
     assert f(ws=None) == -5 and f(wsb=lib.bqm_router_loss_workspace_size(4, 8) - 1) == -5
