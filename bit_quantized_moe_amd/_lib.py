@@ -329,29 +329,29 @@ def bqm_lora_grad(d: MoEDesc, x, dy, ws, dA_gu, dB_gu, dA_dn, dB_dn, stream=None
 # tensors, so the tensors' types, shapes and layout are checked here; everything else is
 # checked behind the C ABI.
 # ----------------------------------------------------------------------------
+_torch = None  # for the checks below, which run several times per call
+
+
 def _dense(name, t, dtype, *shape):
-    """t (None passes) if it is a contiguous GPU tensor of that dtype and number of elements."""
+    """Raises unless t is None or a contiguous tensor of that dtype and number of elements on
+    the current GPU (kernels are launched there)."""
     if t is None:
-        return None
-    if t.dtype is not _dtype(dtype):
+        return
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    if t.dtype is not getattr(_torch, dtype):
         raise BQMError(-1, f"{name}: dtype {t.dtype}, torch.{dtype} needed")
     if not t.is_contiguous():
         raise BQMError(-2, f"{name}: not contiguous")
     if shape and t.numel() != math.prod(shape):
         raise BQMError(-2, f"{name}: shape {tuple(t.shape)}, {shape} needed")
-    if t.get_device() < 0:
+    d = t.get_device()
+    if d < 0:
         raise BQMError(-1, f"{name}: not a GPU tensor")
-    return t
-
-
-_dtypes = {}
-
-
-def _dtype(name):
-    if name not in _dtypes:
-        import torch
-        _dtypes[name] = getattr(torch, name)
-    return _dtypes[name]
+    if d != _torch._C._cuda_getDevice():
+        raise BQMError(-1, f"{name}: on device {d}, the current one is {_torch._C._cuda_getDevice()}")
 
 
 def _mxfp4(name, q: QTensor):
@@ -444,7 +444,8 @@ def bqm_router_loss(logits, topk_idx, valid, counts, loss, ws, stream=None):
     _dense("valid", valid, "uint8", T)
     _dense("counts", counts, "int32", E + 1)
     _dense("loss", loss, "float32", 2)
-    wsb = 0 if ws is None else ws.numel() * ws.element_size()
+    _dense("ws", ws, "uint8")
+    wsb = 0 if ws is None else ws.numel()
     _check(lib.bqm_router_loss(_ptr(logits), _ptr(topk_idx), _ptr(valid), T, E, k, _ptr(counts), _ptr(loss), _ptr(ws),
                                wsb, _stream(stream)))
 

@@ -155,6 +155,9 @@ SHAPES = [  # E, T, k, N, K, kind
     (7, 259, 4, 1056, 160, "dropped"),
     (128, 64, 8, 128, 768, "even"),
     (1024, 40, 2, 64, 64, "even"),
+    (4, 60, 2, 288, 384, "zipf"),
+    (5, 110, 2, 1120, 256, "dropped"),
+    (2, 150, 1, 64, 128, "even"),
 ]
 
 
@@ -268,6 +271,68 @@ def test_products_past_four_gigabytes_of_weights():
         within(host(y[i]), ref, 2.0 ** -8 * np.abs(ref) + K * 2.0 ** -23 * mag, f"y {e}")
         ref, mag = dy[i] @ w, np.abs(dy[i]) @ np.abs(w)
         within(host(dx[i]), ref, 2.0 ** -8 * np.abs(ref) + N * 2.0 ** -23 * mag, f"dx {e}")
+
+
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("gib", [3.5, 4.5])
+def test_products_of_large_activations(gib, gather):
+    """Source rows past 2 and 4 GiB, gathered in a random order or as they lie; a sample of
+    the results against the oracle."""
+    import torch
+    log(f"mxfp4 products, activations of {gib} GiB, gather={gather}")
+    bqm = _bqm()
+    gen = torch.Generator(device=gpu()).manual_seed(3)
+    K, N = 4096, 32
+    R = int(gib * 2 ** 30) // (K // 2)
+    x = bqm.alloc_qtensor(bqm.FMT_MXFP4, 1, R, K)
+    x.codes.random_(0, 256, generator=gen)
+    x.scales.random_(120, 130, generator=gen)
+    w = quantize(bf16(np.random.default_rng(1).standard_normal((2, N, K))))
+    perm = torch.randperm(R, generator=gen, device=gpu()).int() if gather else None
+    off = np.array([0, R // 3, R], np.int32)
+    y = torch.empty((R, N), dtype=torch.bfloat16, device=gpu())
+    bqm.bqm_mxfp4_gemm(x, w, dev(off), perm, 1, y)
+    pos = np.unique(np.concatenate([[0, R // 3 - 1, R // 3, R - 1], np.random.default_rng(2).integers(0, R, 200)]))
+    rows = host(perm[dev(pos)]) if gather else pos
+    e = (pos >= off[1]).astype(int)
+    wv = mx.dequantize_mxfp4(host(w.codes), host(w.scales))
+    xv = mx.dequantize_mxfp4(host(x.codes[0, dev(rows)]), host(x.scales[0, dev(rows)]))
+    ref, mag = (np.stack([f(wv[e[i]]) @ f(xv[i]) for i in range(len(pos))]) for f in (np.asarray, np.abs))
+    within(host(y[dev(pos)]), ref, 2.0 ** -8 * np.abs(ref) + K * 2.0 ** -23 * mag, "y")
+    del x, y
+    K, N = 128, 4096
+    R = int(gib * 2 ** 30) // (2 * N)
+    dy = torch.randn((R, N), generator=gen, device=gpu(), dtype=torch.bfloat16)
+    w = quantize(bf16(np.random.default_rng(1).standard_normal((2, N, K))))
+    perm = torch.randperm(R, generator=gen, device=gpu()).int() if gather else None
+    off = np.array([0, R // 3, R], np.int32)
+    dx = torch.empty((R, K), dtype=torch.bfloat16, device=gpu())
+    bqm.bqm_mxfp4_dgrad(w, dy, dev(off), perm, 1, dx)
+    pos = np.unique(np.concatenate([[0, R // 3 - 1, R // 3, R - 1], np.random.default_rng(2).integers(0, R, 200)]))
+    rows = host(perm[dev(pos)]) if gather else pos
+    e = (pos >= off[1]).astype(int)
+    wv = mx.dequantize_mxfp4(host(w.codes), host(w.scales))
+    dv = host(dy[dev(rows)])
+    ref, mag = (np.stack([f(dv[i]) @ f(wv[e[i]]) for i in range(len(pos))]) for f in (np.asarray, np.abs))
+    within(host(dx[dev(pos)]), ref, 2.0 ** -8 * np.abs(ref) + N * 2.0 ** -23 * mag, "dx")
+
+
+def test_dgrad_is_the_products_difference():
+    """The product is linear, so its differences along the unit vectors are its derivative:
+    rows of one 1 give W's columns, and the gradient of one output W's rows, both exactly."""
+    import torch
+    log("dgrad against the product's differences")
+    bqm = _bqm()
+    rng = np.random.default_rng(8)
+    E, N, K = 3, 160, 96
+    w = quantize(bf16(rng.standard_normal((E, N, K)) * np.exp2(rng.integers(-9, 9, (E, N, 1)).astype(np.float64))))
+    y = torch.empty((E * K, N), dtype=torch.bfloat16, device=gpu())
+    dx = torch.empty((E * N, K), dtype=torch.bfloat16, device=gpu())
+    bqm.bqm_mxfp4_gemm(quantize(np.tile(np.eye(K), (E, 1))[None]), w, dev(np.arange(E + 1, dtype=np.int32) * K), None,
+                       1, y)
+    bqm.bqm_mxfp4_dgrad(w, dev_bf16(np.tile(np.eye(N), (E, 1))), dev(np.arange(E + 1, dtype=np.int32) * N), None, 1,
+                        dx)
+    assert torch.equal(y.reshape(E, K, N).transpose(1, 2), dx.reshape(E, N, K))
 
 
 # ---------------------------------------------------------------------------
@@ -672,3 +737,21 @@ def test_binding_checks_every_tensor():
                 with pytest.raises((bqm.BQMError, ValueError, IndexError)):
                     f(*args[:i], other, *args[i + 1:])
     torch.cuda.synchronize()
+
+
+def test_binding_refuses_another_device_and_host_workspaces(monkeypatch):
+    import torch
+    from bit_quantized_moe_amd import _lib
+    log("binding, device checks")
+    bqm = _bqm()
+    x = torch.zeros((1, 8, 32), dtype=torch.bfloat16, device=gpu())
+    q = bqm.alloc_qtensor(bqm.FMT_MXFP4, 1, 8, 32)
+    l, idx = torch.zeros((4, 8), device=gpu()), torch.zeros((4, 2), dtype=torch.int32, device=gpu())
+    counts, loss = torch.zeros(9, dtype=torch.int32, device=gpu()), torch.zeros(2, device=gpu())
+    with pytest.raises(_lib.BQMError, match="ws: not a GPU tensor"):
+        bqm.bqm_router_loss(l, idx, None, counts, loss, torch.zeros(1 << 16, dtype=torch.uint8))
+    with pytest.raises(_lib.BQMError, match="ws: not contiguous"):
+        bqm.bqm_router_loss(l, idx, None, counts, loss, torch.zeros(1 << 17, dtype=torch.uint8, device=gpu())[::2])
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: x.get_device() + 1)
+    with pytest.raises(_lib.BQMError, match="x: on device"):
+        bqm.bqm_quantize_mxfp4(x, q)
