@@ -500,11 +500,13 @@ struct Tile {
   // Copies of this wave that its wait in slice 3 may leave in flight: those of later steps
   static constexpr int kInFlight = DEEP ? (D - 1) * kOps : 0;
 
-  // other work of slices 0-2, item i: fragment reads of the next slice, then copies and what
-  // becomes of them.  Slice 0: the rest of the next step's copies (DEEP: all of step ks + D's,
-  // whose stage was read in step ks - 1, and the codes of the step after it), and the
-  // forward's scales of the next group (even steps).  Slice 1: dgrad: the next step's codes
-  // are read and half decoded.  Slice 2: scales written, or the rest decoded.
+  // other work of slices 0-2, item i: fragment reads of the next slice, copies and what
+  // becomes of them.  Slice 0: the rest of the next step's copies, before the reads as they
+  // have the least time (64 experts of 1024 rows, 4096 x 6144: product 1046 -> 1013 us,
+  // gradient 2668 -> 2615 us), and the forward's scales of the next group (even steps).  DEEP:
+  // after the reads all copies of step ks + D, whose stage was read in step ks - 1, and the
+  // codes of the step after it.  Slice 1: dgrad: the next step's codes are read and half
+  // decoded.  Slice 2: scales written, or the rest decoded.
   template <int VT, int KK, int LEFT, int PAR>
   static constexpr int items() {
     const int reads = TN + VT;
@@ -516,13 +518,18 @@ struct Tile {
   template <int VT, int KK, int LEFT, int PAR>
   __device__ __forceinline__ void item(int i, int ks, int st) {
     constexpr int k = (KK + 1) & 1;
+    if constexpr (KK == 0 && !DEEP && LEFT > 0) {  // copies first
+      if (i < kCopies - kFirst) return copy(kFirst + i, ks + 1, st ^ 1);
+      i -= kCopies - kFirst;
+    }
     if (i < TN + VT) return read(k, i, KK + 1, stage(ks, st), st);
     i -= TN + VT;
     if constexpr (LEFT > 0) {
       if constexpr (KK == 0) {
-        constexpr int ahead = DEEP ? D : 1;
-        if (i < kCopies - kFirst) return copy(kFirst + i, ks + ahead, stage(ks + ahead, st ^ 1));
-        i -= kCopies - kFirst;
+        if constexpr (DEEP) {
+          if (i < kCopies) return copy(i, ks + D, stage(ks + D, st));
+          i -= kCopies;
+        }
         if constexpr (FWD)
           get_scales(min((ks >> 1) + 1, (nb - 1) >> 4));  // the last group again: it is then not used
         else
@@ -568,7 +575,8 @@ struct Tile {
   }
 
   // slice 3: its first MFMA, then the step's barrier, then slice 0 of the next step is read
-  // and the copies of the step after it begin
+  // and, in turn with those reads, the copies of the step after it begin (12 or all 16 of
+  // them here, not 8, is no faster)
   template <int VT, int LEFT>
   __device__ __forceinline__ void slice3(int ks, int st) {
     constexpr int NP = VT * TN, NR = TN + VT, NW = FWD ? NR : 0;
@@ -589,7 +597,12 @@ struct Tile {
         const uint32_t *sw = nullptr;
         if constexpr (FWD) sw = scale_words(ks + 1);
 #pragma unroll
-        for (int i = q * NI / NP; i < (q + 1) * NI / NP; ++i) {
+        for (int at = q * NI / NP; at < (q + 1) * NI / NP; ++at) {
+          // in turn a copy and a read, as long as there are both
+          constexpr int both = NC < NR + NW ? NC : NR + NW;
+          const bool isc = at < 2 * both ? !(at & 1) : NC > both;
+          const int j0 = at < 2 * both ? at >> 1 : at - both;
+          const int i = isc ? NR + NW + j0 : j0;
           if (i < NR) {
             read(0, i, 0, stage(ks + 1, st ^ 1), st ^ 1);
           } else if (i < NR + NW) {
