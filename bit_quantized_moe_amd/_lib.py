@@ -8,7 +8,6 @@ bit_quantized_moe_amd.build); without it every call raises.
 from __future__ import annotations
 
 import ctypes as C
-import math
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -329,104 +328,99 @@ def bqm_lora_grad(d: MoEDesc, x, dy, ws, dA_gu, dB_gu, dA_dn, dB_dn, stream=None
 # tensors, so the tensors' types, shapes and layout are checked here; everything else is
 # checked behind the C ABI.
 # ----------------------------------------------------------------------------
-_torch = None  # for the checks below, which run several times per call
+_torch = _bf16 = _f32 = _i32 = _u8 = None
 
 
-def _dense(name, t, dtype, *shape):
-    """Raises unless t is None or a contiguous tensor of that dtype and number of elements on
-    the current GPU (kernels are launched there)."""
-    if t is None:
-        return
-    global _torch
+def _begin():
+    """The library and the current device (where kernels are launched; -2 without a GPU)."""
+    global _torch, _bf16, _f32, _i32, _u8
     if _torch is None:
         import torch
-        _torch = torch
-    if t.dtype is not getattr(_torch, dtype):
-        raise BQMError(-1, f"{name}: dtype {t.dtype}, torch.{dtype} needed")
+        _torch, _bf16, _f32, _i32, _u8 = torch, torch.bfloat16, torch.float32, torch.int32, torch.uint8
+    try:
+        return load(), _torch._C._cuda_getDevice()
+    except RuntimeError:
+        return load(), -2
+
+
+def _dense(name, t, dtype, n, dev):
+    """Address of t (None: None) if it is a contiguous tensor of n elements of that dtype on dev.
+    The checks of a short call take as long as its kernel runs, so they are one expression."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.numel() == n and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    name = ".".join(name) if isinstance(name, tuple) else name
+    if t.dtype is not dtype:
+        raise BQMError(-1, f"{name}: dtype {t.dtype}, {dtype} needed")
     if not t.is_contiguous():
         raise BQMError(-2, f"{name}: not contiguous")
-    if shape and t.numel() != math.prod(shape):
-        raise BQMError(-2, f"{name}: shape {tuple(t.shape)}, {shape} needed")
-    d = t.get_device()
-    if d < 0:
+    if t.numel() != n:
+        raise BQMError(-2, f"{name}: shape {tuple(t.shape)}, {n} elements needed")
+    if t.get_device() < 0:
         raise BQMError(-1, f"{name}: not a GPU tensor")
-    if d != _torch._C._cuda_getDevice():
-        raise BQMError(-1, f"{name}: on device {d}, the current one is {_torch._C._cuda_getDevice()}")
+    raise BQMError(-1, f"{name}: on device {t.get_device()}, the current one is {dev}")
 
 
-def _mxfp4(name, q: QTensor):
+def _mxfp4(name, q: QTensor, dev):
     if q.fmt != FMT_MXFP4:
         raise BQMError(-1, f"{name}: format {q.fmt}, FMT_MXFP4 needed")
-    _dense(name + ".codes", q.codes, "uint8", q.n_mat, q.rows, q.cols // 2)
-    _dense(name + ".scales", q.scales, "uint8", q.n_mat, q.rows, q.cols // 32)
-    return q.c()
+    n = q.n_mat * q.rows * q.cols
+    return C.byref(QTensorC(FMT_MXFP4, 0, q.n_mat, q.rows, q.cols, _dense((name, "codes"), q.codes, _u8, n // 2, dev),
+                            _dense((name, "scales"), q.scales, _u8, n // 32, dev), None, 0, 0))
 
 
 def bqm_quantize_mxfp4(x, out: QTensor, stream=None):
     """bf16 x [n_mat, rows, cols] -> out, an MXFP4 stack (returned)."""
-    lib = load()
-    _dense("x", x, "bfloat16", out.n_mat, out.rows, out.cols)
-    qc = _mxfp4("out", out)
-    _check(lib.bqm_quantize_mxfp4(_ptr(x), C.byref(qc), _stream(stream)))
+    lib, dev = _begin()
+    _check(lib.bqm_quantize_mxfp4(_dense("x", x, _bf16, out.n_mat * out.rows * out.cols, dev), _mxfp4("out", out, dev),
+                                  _stream(stream)))
     return out
 
 
 def bqm_mxfp4_gemm(x: QTensor, w: QTensor, offsets, perm, k, y, stream=None):
     """y [R, N] = rows of x [1, rows, K] times their experts' w [E, N, K]; perm None: rows
     are in routed order already.  R is y's first dimension."""
-    lib = load()
+    lib, dev = _begin()
     R = y.shape[0]
-    xc, wc = _mxfp4("x", x), _mxfp4("w", w)
-    _dense("offsets", offsets, "int32", w.n_mat + 1)
-    _dense("perm", perm, "int32", R)
-    _dense("y", y, "bfloat16", R, w.rows)
-    _check(lib.bqm_mxfp4_gemm(C.byref(xc), C.byref(wc), _ptr(offsets), _ptr(perm), k, R, _ptr(y), _stream(stream)))
+    _check(lib.bqm_mxfp4_gemm(_mxfp4("x", x, dev), _mxfp4("w", w, dev), _dense("offsets", offsets, _i32, w.n_mat + 1, dev),
+                              _dense("perm", perm, _i32, R, dev), k, R, _dense("y", y, _bf16, R * w.rows, dev),
+                              _stream(stream)))
     return y
 
 
 def bqm_mxfp4_dgrad(w: QTensor, dy, offsets, perm, k, dx, stream=None):
     """dx [R, K] = rows of dy [rows, N] times their experts' DQ(w) [E, N, K]."""
-    lib = load()
-    R = dx.shape[0]
-    wc = _mxfp4("w", w)
-    _dense("dy", dy, "bfloat16", dy.shape[0], w.rows)
-    _dense("offsets", offsets, "int32", w.n_mat + 1)
-    _dense("perm", perm, "int32", R)
-    _dense("dx", dx, "bfloat16", R, w.cols)
-    _check(lib.bqm_mxfp4_dgrad(C.byref(wc), _ptr(dy), dy.shape[0], _ptr(offsets), _ptr(perm), k, R, _ptr(dx),
-                               _stream(stream)))
+    lib, dev = _begin()
+    R, rows = dx.shape[0], dy.shape[0]
+    _check(lib.bqm_mxfp4_dgrad(_mxfp4("w", w, dev), _dense("dy", dy, _bf16, rows * w.rows, dev), rows,
+                               _dense("offsets", offsets, _i32, w.n_mat + 1, dev), _dense("perm", perm, _i32, R, dev), k,
+                               R, _dense("dx", dx, _bf16, R * w.cols, dev), _stream(stream)))
     return dx
 
 
 def bqm_swiglu_ckpt_fwd(h, h8, h8_scales, a=None, aq: Optional[QTensor] = None, n_rows=None, stream=None):
     """h [R, 2I] -> the 8-bit copy h8 [R, 2I], h8_scales [R, 2I/32]; a [R, I], aq [1, R, I]
     where given.  n_rows: a one-element int32 tensor (offsets[E:], say)."""
-    lib = load()
-    R, I = h.shape[0], h.shape[1] // 2
-    _dense("h", h, "bfloat16", R, 2 * I)
-    _dense("h8", h8, "uint8", R, 2 * I)
-    _dense("h8_scales", h8_scales, "uint8", R, 2 * I // 32)
-    _dense("a", a, "bfloat16", R, I)
-    _dense("n_rows", n_rows, "int32", 1)
-    qc = None if aq is None else C.byref(_mxfp4("aq", aq))
-    _check(lib.bqm_swiglu_ckpt_fwd(_ptr(h), R, I, _ptr(n_rows), _ptr(h8), _ptr(h8_scales), _ptr(a), qc,
+    lib, dev = _begin()
+    R, I2 = h.shape
+    I, n = I2 // 2, R * I2
+    _check(lib.bqm_swiglu_ckpt_fwd(_dense("h", h, _bf16, R * 2 * I, dev), R, I, _dense("n_rows", n_rows, _i32, 1, dev),
+                                   _dense("h8", h8, _u8, n, dev), _dense("h8_scales", h8_scales, _u8, n // 32, dev),
+                                   _dense("a", a, _bf16, R * I, dev), None if aq is None else _mxfp4("aq", aq, dev),
                                    _stream(stream)))
 
 
 def bqm_swiglu_ckpt_bwd(h8, h8_scales, da, perm, topk_w, dh, dtopk_w=None, n_rows=None, stream=None):
     """The 8-bit copy and da [R, I] -> dh [R, 2I], dtopk_w [R] (or [T, k]) where given."""
-    lib = load()
+    lib, dev = _begin()
     R, I = da.shape
-    _dense("h8", h8, "uint8", R, 2 * I)
-    _dense("h8_scales", h8_scales, "uint8", R, 2 * I // 32)
-    _dense("da", da, "bfloat16", R, I)
-    _dense("perm", perm, "int32", R)
-    _dense("topk_w", topk_w, "float32", R)
-    _dense("dh", dh, "bfloat16", R, 2 * I)
-    _dense("dtopk_w", dtopk_w, "float32", R)
-    _dense("n_rows", n_rows, "int32", 1)
-    _check(lib.bqm_swiglu_ckpt_bwd(_ptr(h8), _ptr(h8_scales), _ptr(da), _ptr(perm), _ptr(topk_w), R, I, _ptr(n_rows),
-                                   _ptr(dh), _ptr(dtopk_w), _stream(stream)))
+    n = R * I
+    _check(lib.bqm_swiglu_ckpt_bwd(_dense("h8", h8, _u8, 2 * n, dev), _dense("h8_scales", h8_scales, _u8, 2 * n // 32, dev),
+                                   _dense("da", da, _bf16, n, dev), _dense("perm", perm, _i32, R, dev),
+                                   _dense("topk_w", topk_w, _f32, R, dev), R, I, _dense("n_rows", n_rows, _i32, 1, dev),
+                                   _dense("dh", dh, _bf16, 2 * n, dev), _dense("dtopk_w", dtopk_w, _f32, R, dev),
+                                   _stream(stream)))
     return dh
 
 
@@ -436,32 +430,22 @@ def bqm_router_loss_workspace_size(T, E) -> int:
 
 def bqm_router_loss(logits, topk_idx, valid, counts, loss, ws, stream=None):
     """logits [T, E], topk_idx [T, k] (valid uint8 [T] or None) -> counts int32 [E+1], loss
-    float32 [2] = (balance loss, z-loss)."""
-    lib = load()
+    float32 [2] = (balance loss, z-loss).  ws: uint8, bqm_router_loss_workspace_size(T, E)."""
+    lib, dev = _begin()
     (T, E), k = logits.shape, topk_idx.shape[1]
-    _dense("logits", logits, "float32")
-    _dense("topk_idx", topk_idx, "int32", T, k)
-    _dense("valid", valid, "uint8", T)
-    _dense("counts", counts, "int32", E + 1)
-    _dense("loss", loss, "float32", 2)
-    _dense("ws", ws, "uint8")
     wsb = 0 if ws is None else ws.numel()
-    _check(lib.bqm_router_loss(_ptr(logits), _ptr(topk_idx), _ptr(valid), T, E, k, _ptr(counts), _ptr(loss), _ptr(ws),
-                               wsb, _stream(stream)))
+    _check(lib.bqm_router_loss(_dense("logits", logits, _f32, T * E, dev), _dense("topk_idx", topk_idx, _i32, T * k, dev),
+                               _dense("valid", valid, _u8, T, dev), T, E, k, _dense("counts", counts, _i32, E + 1, dev),
+                               _dense("loss", loss, _f32, 2, dev), _dense("ws", ws, _u8, wsb, dev), wsb, _stream(stream)))
 
 
 def bqm_router_grad(logits, topk_idx, valid, counts, dtopk_w, dloss, renorm, dlogits, stream=None):
     """dlogits [T, E] of the losses (times dloss [2], or None) and of topk_w (times dtopk_w
     [T, k], or None)."""
-    lib = load()
+    lib, dev = _begin()
     (T, E), k = logits.shape, topk_idx.shape[1]
-    _dense("logits", logits, "float32")
-    _dense("topk_idx", topk_idx, "int32", T, k)
-    _dense("valid", valid, "uint8", T)
-    _dense("counts", counts, "int32", E + 1)
-    _dense("dtopk_w", dtopk_w, "float32", T, k)
-    _dense("dloss", dloss, "float32", 2)
-    _dense("dlogits", dlogits, "float32", T, E)
-    _check(lib.bqm_router_grad(_ptr(logits), _ptr(topk_idx), _ptr(valid), _ptr(counts), _ptr(dtopk_w), _ptr(dloss), T,
-                               E, k, int(renorm), _ptr(dlogits), _stream(stream)))
+    _check(lib.bqm_router_grad(_dense("logits", logits, _f32, T * E, dev), _dense("topk_idx", topk_idx, _i32, T * k, dev),
+                               _dense("valid", valid, _u8, T, dev), _dense("counts", counts, _i32, E + 1, dev),
+                               _dense("dtopk_w", dtopk_w, _f32, T * k, dev), _dense("dloss", dloss, _f32, 2, dev), T, E, k,
+                               int(renorm), _dense("dlogits", dlogits, _f32, T * E, dev), _stream(stream)))
     return dlogits

@@ -155,19 +155,25 @@ struct LossWs {
 constexpr int kFinE = 32;  // experts per workgroup of the finishing kernel
 
 struct LossGeom {
-  int G;        // workgroups of the first kernel
+  int G;  // workgroups of the first kernel
   size_t bytes;
 };
 
+// lanes that hold a token's logits, 4 each up to 256 experts
+int lanes_of(int E) { return E <= 16 ? 4 : E <= 32 ? 8 : E <= 64 ? 16 : E <= 128 ? 32 : 64; }
+
 // Workgroups of 16 waves, two per CU at most: 32 waves keep enough rows in flight (with 8
 // waves per CU the 131072 x 256 batch took 62 us, with 32 and the next row in flight 34 us,
-// 4.0 TB/s).  A workgroup takes at
-// least kTokMin tokens, so that a small batch writes few partial sums.
+// 4.0 TB/s).  A workgroup takes at least kTokMin tokens, so that a small batch writes few
+// partial sums.  A batch of at most kOneTurns tokens per group of lanes goes to one
+// workgroup, which forms the losses itself and saves the finishing kernel: a turn takes
+// 0.8 us, the two kernels 8.3 us at 8 experts, 9.1 at 60, 12.7 at 256 and 21.6 at 1024 (one
+// with 8 turns: 9.6, 10.1, 10.7 and 20.4 us), and a launch costs the host 3.3 us.
 constexpr int kSumThreads = 1024, kSumWaves = kSumThreads / 64;
-constexpr int64_t kTokMin = 64;
+constexpr int64_t kTokMin = 64, kOneTurns = 8;
 LossGeom loss_geom(int64_t T, int32_t E) {
-  int64_t G = cdiv(T, kTokMin);
-  G = G < 1 ? 1 : (G > 512 ? 512 : G);
+  int64_t G = T <= kOneTurns * (kSumThreads / lanes_of(E)) ? 1 : cdiv(T, kTokMin);
+  G = G > 512 ? 512 : G;
   LossGeom g;
   g.G = (int)G;
   g.bytes = align256((size_t)G * E * 4) * 2 + align256((size_t)G * 4) * 2 + align256(kMaxE / kFinE * sizeof(double)) + 256;
@@ -191,11 +197,20 @@ LossWs loss_ws(void *ws, int G, int E) {
   return w;
 }
 
+// the losses from sum_e c_e P_e n and sum_t lse^2 over the n tokens that count
+__device__ __forceinline__ void write_losses(int E, int k, int32_t n, double b, double z, int32_t *counts, float *loss) {
+  const double nn = (double)n;
+  counts[E] = n;
+  loss[0] = n > 0 ? (float)((double)E * b / (nn * nn * (double)k)) : 0.0f;
+  loss[1] = n > 0 ? (float)(z / nn) : 0.0f;
+}
+
 template <int L, int NV, bool VEC>
 __global__ void __launch_bounds__(kSumThreads) router_sums(const float *__restrict__ logits,
                                                         const int32_t *__restrict__ idx,
                                                         const uint8_t *__restrict__ valid, int64_t T, int E, int k,
-                                                        LossWs w) {
+                                                        LossWs w, int32_t *__restrict__ counts,
+                                                        float *__restrict__ loss) {
   constexpr int kGroups = kSumThreads / L;
   extern __shared__ float ps[];  // [kSumWaves][E]: the waves' sums
   __shared__ int32_t hist[kMaxE];
@@ -271,12 +286,28 @@ __global__ void __launch_bounds__(kSumThreads) router_sums(const float *__restri
       }
   }
   __syncthreads();
-  for (int e = tid; e < E; e += kSumThreads) {
-    float p = 0.0f;
+  const bool one = gridDim.x == 1;
+  float p = 0.0f;
+  if (tid < E) {  // E <= kSumThreads
 #pragma unroll
-    for (int q = 0; q < kSumWaves; ++q) p += ps[q * E + e];
-    w.psum[(int64_t)blockIdx.x * E + e] = p;
-    w.counts[(int64_t)blockIdx.x * E + e] = hist[e];
+    for (int q = 0; q < kSumWaves; ++q) p += ps[q * E + tid];
+    if (one) {
+      counts[tid] = hist[tid];
+    } else {
+      w.psum[(int64_t)blockIdx.x * E + tid] = p;
+      w.counts[(int64_t)blockIdx.x * E + tid] = hist[tid];
+    }
+  }
+  double b = 0.0;
+  if (one) {  // sum_e c_e P_e: a butterfly in each wave, then the waves in order
+    __shared__ double bs[kSumWaves];
+    b = tid < E ? (double)hist[tid] * (double)p : 0.0;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) b += __shfl_xor(b, m, 64);
+    if (lane == 0) bs[wave] = b;
+    __syncthreads();
+    b = 0.0;
+    for (int q = 0; q < kSumWaves; ++q) b += bs[q];
   }
   if (tid == 0) {
     float zt = 0.0f;
@@ -285,8 +316,12 @@ __global__ void __launch_bounds__(kSumThreads) router_sums(const float *__restri
       zt += zs[q];
       nt += ns[q];
     }
-    w.z[blockIdx.x] = zt;
-    w.n[blockIdx.x] = nt;
+    if (one) {
+      write_losses(E, k, nt, b, (double)zt, counts, loss);
+    } else {
+      w.z[blockIdx.x] = zt;
+      w.n[blockIdx.x] = nt;
+    }
   }
 }
 
@@ -355,10 +390,7 @@ __global__ void __launch_bounds__(kFinThreads) router_finish(LossWs w, int G, in
     double b = 0.0;
     for (unsigned q = 0; q < gridDim.x; ++q)
       b += __hip_atomic_load(&w.part[q], __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_AGENT);
-    const double nn = (double)ns[0];
-    counts[E] = ns[0];
-    loss[0] = ns[0] > 0 ? (float)((double)E * b / (nn * nn * (double)k)) : 0.0f;
-    loss[1] = ns[0] > 0 ? (float)(zs[0] / nn) : 0.0f;
+    write_losses(E, k, ns[0], b, zs[0], counts, loss);
   }
 }
 
@@ -553,15 +585,13 @@ void with_shape(int E, F f) {
       f(L, NV, std::false_type{});
   };
   using std::integral_constant;
-  if (E <= 16)
-    vec(integral_constant<int, 4>{}, integral_constant<int, 1>{});
-  else if (E <= 32)
-    vec(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-  else if (E <= 64)
-    vec(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-  else if (E <= 128)
-    vec(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-  else if (E <= 256)
+  switch (lanes_of(E)) {
+    case 4: return vec(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+    case 8: return vec(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+    case 16: return vec(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+    case 32: return vec(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  }
+  if (E <= 256)
     vec(integral_constant<int, 64>{}, integral_constant<int, 1>{});
   else if (E <= 512)
     vec(integral_constant<int, 64>{}, integral_constant<int, 2>{});
@@ -596,10 +626,11 @@ extern "C" bqm_status bqm_router_loss(const float *logits, const int32_t *topk_i
   const LossWs w = loss_ws(ws, g.G, E);
   hipStream_t s = as_stream(stream);
   with_shape(E, [&](auto L, auto NV, auto VEC) {
-    router_sums<L.value, NV.value, VEC.value><<<g.G, kSumThreads, kSumWaves * E * sizeof(float), s>>>(logits, topk_idx, valid, T, E, k, w);
+    router_sums<L.value, NV.value, VEC.value><<<g.G, kSumThreads, kSumWaves * E * sizeof(float), s>>>(
+        logits, topk_idx, valid, T, E, k, w, counts, loss);
   });
   st = launch_status("router_sums");
-  if (st != BQM_OK) return st;
+  if (st != BQM_OK || g.G == 1) return st;
   router_finish<<<(unsigned)cdiv(E, kFinE), kFinThreads, 0, s>>>(w, g.G, E, k, counts, loss);
   return launch_status("router_finish");
 }
