@@ -732,12 +732,32 @@ struct Tile {
                          pack_bf16_rne(acc[tm][tn][4 * q + 2], acc[tm][tn][4 * q + 3]));
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // store i takes RP rows of the wave's from RP i on; lane l holds chunk l % CH of row l / CH
+    // of them.  Only lane offsets are vector arithmetic (32 rows of the output, below 2 GiB),
+    // and eight reads are in flight at a time: addresses formed in full for each store, and
+    // a wait for each read, cost 6 us per tile of 256 x 256.
+    constexpr int RP = 64 / CH, NS8 = VT * CH / 2;
+    const int lr = lane / CH, c = lane & (CH - 1);
+    const uint32_t off = ((uint32_t)lr * ncols + 8 * c) * 2;
+    const int n = n0 + 32 * wn * TN;  // the wave's first column
+    const bool in = n + 8 * c < ncols;
+    const int left = rows - 32 * wm - lr;
+    const uint8_t *base = uniform(p.out + (row_base + 32 * wm) * ncols + n);
 #pragma unroll
-    for (int i = 0; i < VT * CH / 2; ++i) {
-      const int at = 64 * i + lane, r = at / CH, c = at % CH;
-      const int row = 32 * (WM * (r >> 5) + wm) + (r & 31), n = n0 + 32 * wn * TN + 8 * c;
-      const u32x4 v = *reinterpret_cast<const u32x4 *>(t + 16 * (r * CH + (c ^ (r & (CH - 1)))));
-      if (row < rows && n < ncols) *reinterpret_cast<u32x4 *>(p.out + (row_base + row) * ncols + n) = v;
+    for (int i0 = 0; i0 < NS8; i0 += 8) {
+      u32x4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8 && i0 + j < NS8; ++j) {
+        const int r0 = RP * (i0 + j);
+        v[j] = *reinterpret_cast<const u32x4 *>(t + 16 * CH * r0 + 16 * CH * lr +
+                                                16 * (c ^ (lr & (CH - 1)) ^ (r0 & (CH - 1))));
+      }
+#pragma unroll
+      for (int j = 0; j < 8 && i0 + j < NS8; ++j) {
+        const int r0 = RP * (i0 + j), row = 32 * WM * (r0 >> 5) + (r0 & 31);
+        if (in && row < left)
+          *reinterpret_cast<u32x4 *>(const_cast<uint8_t *>(base + (int64_t)row * ncols * 2 + off)) = v[j];
+      }
     }
   }
 
@@ -766,7 +786,8 @@ __global__ void __launch_bounds__(NTHR, OCC) mx_tiles(MxParams p) {
     map.find(mt, sm.found);
     barrier_lds();  // also: the stages of the tile before are free
     const int e = __builtin_amdgcn_readfirstlane(sm.found[0]);
-    const int rb = seg_at(p, e), n_e = seg_at(p, e + 1) - rb;
+    const int rb = __builtin_amdgcn_readfirstlane(seg_at(p, e));
+    const int n_e = __builtin_amdgcn_readfirstlane(seg_at(p, e + 1)) - rb;
     const int m0 = (mt - __builtin_amdgcn_readfirstlane(sm.found[1])) * BM;
     const int rows = min(n_e - m0, BM);
     const int vt = (rows + 32 * WM - 1) / (32 * WM);  // row tiles per wave that hold rows
