@@ -775,14 +775,20 @@ __global__ void __launch_bounds__(NTHR, OCC) mx_tiles(MxParams p) {
   __shared__ __attribute__((aligned(16))) Smem<BM, BN, FWD, NS> sm;
   const int ncols = FWD ? p.N : p.K;
   TileMap map;
-  const int total = map.build<BM>(p, sm.wsum) * p.NT;
+  const int mtiles = map.build<BM>(p, sm.wsum), total = mtiles * p.NT;
   // each XCD (workgroups b % 8) walks a contiguous range of tiles, so that the tiles in
-  // flight there share an expert's rows and weights in its L2
+  // flight there share an expert's rows and weights in its L2.  GM row tiles are walked
+  // together, column tile by column tile: the 32 largest tiles that an XCD has in flight are
+  // then 4 x 8 and not 2 x 16 of them (64 experts of 1024 rows, 4096 x 6144: product reads
+  // 1.96 -> 1.30 GB and takes 958 -> 940 us, gradient 3.43 -> 2.56 GB, 2521 -> 2478 us; 2 or 8
+  // row tiles gain less, and the smaller tiles lose 1%)
+  constexpr int GM = TM == 4 ? 4 : 1;
   const int per = (total + 7) / 8;
   const int first = (blockIdx.x & 7) * per, last = min(first + per, total);
   T t(p, sm);
   for (int L = first + (int)(blockIdx.x >> 3); L < last; L += (int)(gridDim.x >> 3)) {
-    const int mt = L / p.NT, n0 = (L % p.NT) * BN;
+    const int m_first = L / (GM * p.NT) * GM, gm = min(GM, mtiles - m_first), in_group = L - m_first * p.NT;
+    const int mt = m_first + in_group % gm, n0 = in_group / gm * BN;
     map.find(mt, sm.found);
     barrier_lds();  // also: the stages of the tile before are free
     const int e = __builtin_amdgcn_readfirstlane(sm.found[0]);
