@@ -142,13 +142,14 @@ struct TileMap {
     return total;
   }
 
-  // the owner of row tile mt writes its expert and that expert's first tile to found
+  // the owner of row tile mt writes its expert, that expert's first tile and number of tiles to found
   __device__ __forceinline__ void find(int mt, int *found) const {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       if (first[i] <= mt && mt < first[i + 1]) {
         found[0] = (int)threadIdx.x * PER + i;
         found[1] = first[i];
+        found[2] = first[i + 1] - first[i];
       }
   }
 };
@@ -196,7 +197,7 @@ struct Smem<BM, BN, true, 2> {
   uint8_t a[2][BM * 128];
   uint8_t b[2][BN * 128];
   uint32_t s[2][2][2][BM + BN + 4];  // [group parity][step of the group][half][row]
-  int wsum[NTHR / 64], found[2];
+  int wsum[NTHR / 64], found[3];
 };
 template <int BM, int BN, int NS>
 struct Smem<BM, BN, false, NS> {
@@ -204,7 +205,7 @@ struct Smem<BM, BN, false, NS> {
   uint16_t dq[2][BN / 64][DK * DQS];
   uint8_t c[NS][DK * 128];           // codes of a step's weight rows, 256 columns
   uint32_t cs[NS][BN / 32 * DK];     // their scales: FAST [row][4 words, of which 2 hold bytes], else [block][row]
-  int wsum[NTHR / 64], found[2];
+  int wsum[NTHR / 64], found[3];
 };
 
 // The scales of blocks 16 g .. 16 g + 15 of a row of nb >= 16 blocks in one load; the last
@@ -775,26 +776,34 @@ __global__ void __launch_bounds__(NTHR, OCC) mx_tiles(MxParams p) {
   __shared__ __attribute__((aligned(16))) Smem<BM, BN, FWD, NS> sm;
   const int ncols = FWD ? p.N : p.K;
   TileMap map;
-  const int mtiles = map.build<BM>(p, sm.wsum), total = mtiles * p.NT;
+  const int total = map.build<BM>(p, sm.wsum) * p.NT;
   // each XCD (workgroups b % 8) walks a contiguous range of tiles, so that the tiles in
-  // flight there share an expert's rows and weights in its L2.  GM row tiles are walked
-  // together, column tile by column tile: the 32 largest tiles that an XCD has in flight are
-  // then 4 x 8 and not 2 x 16 of them (64 experts of 1024 rows, 4096 x 6144: product reads
-  // 1.96 -> 1.30 GB and takes 958 -> 940 us, gradient 3.43 -> 2.56 GB, 2521 -> 2478 us; 2 or 8
-  // row tiles gain less, and the smaller tiles lose 1%)
+  // flight there share an expert's rows and weights in its L2.  In the largest tile's kernels
+  // an expert's row tiles are walked in groups of about GM, column tile by column tile: the 32
+  // tiles that an XCD has in flight are then 4 x 8 and not 2 x 16 of them (64 experts of 1024
+  // rows, 4096 x 6144: product reads 1.96 -> 1.30 GB and takes 958 -> 940 us, gradient 3.43 ->
+  // 2.56 GB, 2521 -> 2478 us; 2 or 8 row tiles gain less, and the smaller tiles lose 1%).  The
+  // groups are even and end with the expert: groups of four across experts made the product
+  // of 64 experts of 950 to 1100 rows read 2.7 GB, not 1.9, in 1069 us, not 1009.
   constexpr int GM = TM == 4 ? 4 : 1;
   const int per = (total + 7) / 8;
   const int first = (blockIdx.x & 7) * per, last = min(first + per, total);
   T t(p, sm);
   for (int L = first + (int)(blockIdx.x >> 3); L < last; L += (int)(gridDim.x >> 3)) {
-    const int m_first = L / (GM * p.NT) * GM, gm = min(GM, mtiles - m_first), in_group = L - m_first * p.NT;
-    const int mt = m_first + in_group % gm, n0 = in_group / gm * BN;
-    map.find(mt, sm.found);
+    map.find(L / p.NT, sm.found);
     barrier_lds();  // also: the stages of the tile before are free
     const int e = __builtin_amdgcn_readfirstlane(sm.found[0]);
     const int rb = __builtin_amdgcn_readfirstlane(seg_at(p, e));
     const int n_e = __builtin_amdgcn_readfirstlane(seg_at(p, e + 1)) - rb;
-    const int m0 = (mt - __builtin_amdgcn_readfirstlane(sm.found[1])) * BM;
+    const int in_e = L - __builtin_amdgcn_readfirstlane(sm.found[1]) * p.NT;  // among the expert's tiles
+    int mt = in_e / p.NT, nt = in_e % p.NT;
+    if constexpr (GM > 1) {  // n_g groups of g row tiles, the last of them of what is left
+      const int c = __builtin_amdgcn_readfirstlane(sm.found[2]), n_g = max((c + GM / 2) / GM, 1), g = (c + n_g - 1) / n_g;
+      const int m_first = in_e / (g * p.NT) * g, gm = min(g, c - m_first), in_g = in_e - m_first * p.NT;
+      mt = m_first + in_g % gm;
+      nt = in_g / gm;
+    }
+    const int m0 = mt * BM, n0 = nt * BN;
     const int rows = min(n_e - m0, BM);
     const int vt = (rows + 32 * WM - 1) / (32 * WM);  // row tiles per wave that hold rows
     t.setup(e, rb, m0, n_e, n0);
