@@ -10,7 +10,8 @@
 // Both kernels are bound by HBM: forward 4 + 2 + 2.06 bytes per element of a, backward
 // 2.06 + 2 + 4.  A lane holds 8 consecutive elements of a row's g and the same 8 of its u
 // (16-byte loads and stores), so a quad of lanes shares a block of each and finds its
-// maximum with two quad-permute moves.
+// maximum with two quad-permute moves.  131072 x 2048: forward 350 us, backward 355 us, 6.1
+// to 6.2 TB/s; 808 x 768: 4 and 5 us, of which a launch with no work is 2.
 #include "common.h"
 
 namespace bqm {

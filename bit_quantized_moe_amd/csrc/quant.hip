@@ -597,7 +597,8 @@ __global__ void __launch_bounds__(kThreads) nf4_dequant(const uint32_t *__restri
 //
 // Bound by HBM: 2.53 bytes per element in each direction.  One lane per 8 elements as
 // in the kernels above, so a quad of lanes shares a block: its maximum is two
-// quad-permute moves, with no LDS and no barrier.
+// quad-permute moves, with no LDS and no barrier.  48 x 4096 x 6144: 492 us and 515 us, 6.2
+// and 5.9 TB/s.
 constexpr uint32_t kE8M0NaN = 255u;
 
 // maximum over the four lanes of a quad
