@@ -247,6 +247,11 @@ def bqm_nf4_nest(plain: QTensor, nested: QTensor, stream=None):
 
 
 def bqm_dequantize(q: QTensor, y, stream=None):
+    if q.fmt == FMT_MXFP4:      # checked as the other MXFP4 calls check theirs
+        lib, dev = _begin()
+        _check(lib.bqm_dequantize(_mxfp4("q", q, dev), _dense("y", y, _bf16, q.n_mat * q.rows * q.cols, dev),
+                                  _stream(stream)))
+        return y
     lib = load()
     qc = q.c()
     _check(lib.bqm_dequantize(C.byref(qc), _ptr(y), _stream(stream)))

@@ -132,3 +132,26 @@ def test_binding_checks_types_shapes_and_layout():
     for what, f in bad:
         with pytest.raises(bqm.BQMError, match=what):
             f()
+
+
+def test_dequantize_of_mxfp4_checks_its_tensors(monkeypatch):
+    """An output of another size, type or layout, or codes of another size, are refused before
+    anything is launched."""
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)  # noqa: E731
+    q = bqm.alloc_qtensor(bqm.FMT_MXFP4, 2, 8, 64, device="cpu")
+    short = bqm.alloc_qtensor(bqm.FMT_MXFP4, 2, 8, 64, device="cpu")
+    short.codes = short.codes[:1].clone()
+    few = bqm.alloc_qtensor(bqm.FMT_MXFP4, 2, 8, 64, device="cpu")
+    few.scales = few.scales[..., :1].clone()
+    with pytest.raises(bqm.BQMError, match="not a GPU tensor"):
+        bqm.bqm_dequantize(q, z(2, 8, 64))
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1)    # host tensors pass the device check
+    for what, f in [
+        ("y: shape", lambda: bqm.bqm_dequantize(q, z(1, 8, 64))),
+        ("y: dtype", lambda: bqm.bqm_dequantize(q, z(2, 8, 64, dtype=torch.float32))),
+        ("y: not contiguous", lambda: bqm.bqm_dequantize(q, z(2, 64, 8).transpose(1, 2))),
+        ("codes: shape", lambda: bqm.bqm_dequantize(short, z(2, 8, 64))),
+        ("scales: shape", lambda: bqm.bqm_dequantize(few, z(2, 8, 64))),
+    ]:
+        with pytest.raises(bqm.BQMError, match=what):
+            f()
