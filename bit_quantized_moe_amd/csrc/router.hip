@@ -506,7 +506,8 @@ __global__ void __launch_bounds__(kThreads) router_grad(const float *__restrict_
         f32x4 mult[NV] = {};
         for (int j = 0; j < k; ++j) {
           const int i = idx[t * k + j];
-          const float d = dw[t * k + j];
+          // an index from E on may name a slot that no expert has: its dw, which can be anything, counts for none
+          const float d = (unsigned)i < (unsigned)E ? dw[t * k + j] : 0.0f;
 #pragma unroll
           for (int v = 0; v < NV; ++v)
 #pragma unroll

@@ -281,7 +281,8 @@ bqm_status bqm_router_loss(const float *logits, const int32_t *topk_idx, const u
  * (device f32 [2], NULL: no loss) plus sum dtopk_w[t, j] topk_w[t, j] (f32 [T, k], NULL:
  * none; topk_w as bqm_route gives it with the same renorm), with the indices and counts
  * held constant.  counts: as bqm_router_loss wrote them for these tokens.  Tokens that do
- * not count get zeros, and their logits and dtopk_w may hold anything. */
+ * not count get zeros, and their logits and dtopk_w may hold anything, as may the dtopk_w of
+ * pairs whose index lies outside [0, E). */
 bqm_status bqm_router_grad(const float *logits, const int32_t *topk_idx, const uint8_t *valid, const int32_t *counts,
                            const float *dtopk_w, const float *dloss, int64_t T, int32_t E, int32_t k, int32_t renorm,
                            float *dlogits, void *stream);

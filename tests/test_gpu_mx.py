@@ -529,6 +529,29 @@ def test_router_against_oracle(T, E, k, renorm, padded, masked, odd):
         within(host(out), g, 2.0 ** -18 * size + 1e-30, "dlogits of one")
 
 
+@pytest.mark.parametrize("E,k", [(3, 2), (13, 3), (21, 4), (37, 4), (60, 8), (100, 16), (250, 8), (1000, 4)])
+def test_router_gradient_ignores_what_dropped_pairs_hold(E, k):
+    """Indices outside [0, E), those among them that fall on a lane's unused places, with
+    NaN and infinite gradients: the result is that of no gradient there."""
+    import torch
+    log(f"router, dropped pairs E={E} k={k}")
+    T = 70
+    l, idx, dw, _ = router_case(T, E, k, False, 0, False)
+    rng = np.random.default_rng(E)
+    drop = rng.random((T, k)) < 0.4
+    beyond = np.array([-1, -E, E, E + 1, E + 2, E + 3, 1 << 30, -(1 << 31)])
+    idx[drop] = beyond[rng.integers(0, len(beyond), drop.sum())]
+    clean = np.where(drop, np.float32(0), dw)
+    dw[drop] = np.array([np.nan, np.inf, -np.inf], np.float32)[rng.integers(0, 3, drop.sum())]
+    dloss = np.array([0.5, 0.25], np.float32)
+    for renorm in (False, True):
+        c, _, out = run_router(l, idx, dw, None, dloss, renorm)
+        _, _, want = run_router(l, idx, clean, None, dloss, renorm)
+        assert torch.equal(out, want)
+        g, size = mx.router_grad(l, idx, None, host(c), clean, dloss.astype(np.float64), renorm)
+        within(host(out), g, 2.0 ** -18 * size + 1e-30, "dlogits")
+
+
 def test_router_batches_of_nothing():
     log("router, no tokens that count")
     E, k = 12, 2
