@@ -116,7 +116,8 @@ __device__ __forceinline__ void load_row(const float *__restrict__ row, int E, i
 }
 
 // x <- e^(x - base), base the row's maximum (0 for a row of nothing but -inf); returns 1 / sum
-// and the row's lse (both 0 for such a row)
+// and the row's lse (both 0 for such a row, whose sum alone is 0: a row of -inf and NaN has a
+// maximum of -inf too, as fmaxf passes NaN over, and its lse is NaN)
 template <int L, int NV>
 __device__ __forceinline__ float softmax_row(f32x4 (&x)[NV], float &lse, float &base) {
   float m = -INFINITY;
@@ -133,7 +134,7 @@ __device__ __forceinline__ float softmax_row(f32x4 (&x)[NV], float &lse, float &
       s += x[v][c];
     }
   s = group_sum<L>(s);
-  lse = m == -INFINITY ? 0.0f : m + logf(s);
+  lse = s == 0.0f ? 0.0f : m + logf(s);
   return s > 0.0f ? 1.0f / s : 0.0f;
 }
 

@@ -269,7 +269,8 @@ bqm_status bqm_swiglu_ckpt_bwd(const uint8_t *h8, const uint8_t *h8_scales, cons
  * (both 0 when n = 0).  counts i32 [E+1]: routed pairs per expert, then n.  Pairs whose
  * index lies outside [0, E) count for no expert; an index that occurs twice in a token
  * counts twice.  -inf logits are experts that are switched off; a token with no other
- * logit has p = 0 and logsumexp 0.  Logits of tokens that do not count may hold anything.
+ * logit has p = 0 and logsumexp 0.  A NaN logit of a token that counts makes both losses
+ * NaN.  Logits of tokens that do not count may hold anything.
  * logits f32 [T, E], topk_idx i32 [T, k]; limits as for bqm_route, T * k < 2^31.  Sums of
  * p are FP32 per workgroup and FP64 across, in a fixed order.  ws:
  * bqm_router_loss_workspace_size() bytes; calls that share one must not overlap. */

@@ -552,6 +552,30 @@ def test_router_gradient_ignores_what_dropped_pairs_hold(E, k):
         within(host(out), g, 2.0 ** -18 * size + 1e-30, "dlogits")
 
 
+@pytest.mark.parametrize("E", [5, 16, 30, 60, 128, 200, 256, 512, 1000])
+@pytest.mark.parametrize("row", ["nan", "nan_and_off", "some"])
+def test_router_losses_show_nan_logits(E, row):
+    """A token that counts with NaN among its logits, whatever the others are (nothing but NaN,
+    NaN and switched-off experts, finite ones): both losses are NaN, as their sums are, and so
+    are the gradients of its logits; those of the other tokens' are not."""
+    log(f"router, NaN logits E={E} {row}")
+    T, k = 9, 2
+    l, idx, dw, _ = router_case(T, E, k, False, 0, False)
+    if row == "nan":
+        l[4] = np.nan
+    elif row == "nan_and_off":
+        l[4] = -np.inf
+        l[4, E // 2] = np.nan
+    else:
+        l[4, E // 2] = np.nan
+    c, loss, out = run_router(l, idx, dw, None, np.ones(2, np.float32), False)
+    assert host(c)[E] == T and np.isnan(host(loss)).all(), host(loss)
+    nan = np.isnan(host(out)).all(1)
+    assert nan[4] and not np.isnan(host(out)[np.arange(T) != 4]).any()
+    c, loss, out = run_router(l, idx, dw, (np.arange(T) != 4).astype(np.uint8), np.ones(2, np.float32), False)
+    assert np.isfinite(host(loss)).all() and np.isfinite(host(out)).all()
+
+
 def test_router_batches_of_nothing():
     log("router, no tokens that count")
     E, k = 12, 2
