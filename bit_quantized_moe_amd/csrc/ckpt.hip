@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_ckpt_bwd(const uint8_t *__res
         const float g = gp[j] * gs, u = up[j] * us;
         const float dv = j ? bf16_hi(d[i]) : bf16_lo(d[i]);
         const float s = sigmoid_f(g), gsg = g * s;
-        dot += dv * gsg * u;
+        dot += dv * (gsg * u);  // da times a: da silu(g) can overflow where a and the sum are finite
         const float wd = w * dv;
         dgv[j] = wd * (u * s) * (1.0f + g * (1.0f - s));
         duv[j] = wd * gsg;

@@ -430,6 +430,27 @@ def test_swiglu_without_perm_weights_or_their_gradient():
     assert torch.equal(dh, dh2)
 
 
+def test_swiglu_weight_gradient_of_large_factors():
+    """da, g and u far apart in size, with a = silu(g) u and da a in the middle of the range:
+    dtopk_w is the sum of da a, not an overflow of da silu(g) (above 2^129 each here)."""
+    import torch
+    log("swiglu, dtopk_w of large factors")
+    bqm = _bqm()
+    R, I = 3, 64
+    g, u, da = (np.zeros((R, I)) for _ in range(3))
+    g[0], u[0], da[0] = 2.0 ** 20, 2.0 ** -120, 2.0 ** 110
+    g[1], u[1], da[1] = 40.0, 2.0 ** -100, 2.0 ** 124
+    g[2], u[2], da[2] = 24.0, 2.0 ** -90, 1.5 * 2.0 ** 127
+    da[:, ::3] *= -1
+    h = np.concatenate([g, u], 1)
+    h8, s8, a, dh = swiglu_buffers(R, I)
+    dw = torch.empty(R, device=gpu())
+    bqm.bqm_swiglu_ckpt_fwd(dev_bf16(h), h8, s8, a=a)
+    bqm.bqm_swiglu_ckpt_bwd(h8, s8, dev_bf16(da), None, dev(np.full(R, 2.0 ** -40, np.float32)), dh, dw)
+    check_swiglu(h, da, np.full(R, 2.0 ** -40), np.arange(R), R, h8, s8, a, dh, dw)
+    assert np.isfinite(host(dw)).all()
+
+
 def test_swiglu_every_block_maximum():
     """All bf16 magnitudes as a block's maximum, in the gate half and in the up half."""
     log("checkpoint block maxima")
