@@ -165,15 +165,17 @@ int lanes_of(int E) { return E <= 16 ? 4 : E <= 32 ? 8 : E <= 64 ? 16 : E <= 128
 
 // Workgroups of 16 waves, two per CU at most: 32 waves keep enough rows in flight (with 8
 // waves per CU the 131072 x 256 batch took 62 us, with 32 and the next row in flight 34 us,
-// 4.0 TB/s).  A workgroup takes at least kTokMin tokens, so that a small batch writes few
-// partial sums.  A batch of at most kOneTurns tokens per group of lanes goes to one
-// workgroup, which forms the losses itself and saves the finishing kernel: a turn takes
-// 0.8 us, the two kernels 8.3 us at 8 experts, 9.1 at 60, 12.7 at 256 and 21.6 at 1024 (one
-// with 8 turns: 9.6, 10.1, 10.7 and 20.4 us), and a launch costs the host 3.3 us.
+// 4.0 TB/s).  One workgroup per kTokMin tokens, so that a small batch writes few partial
+// sums, but no more than get a token: with 32 experts or fewer a workgroup's groups of lanes
+// take 128 or 256 tokens in one turn.  A batch of at most kOneTurns tokens per group of lanes
+// goes to one workgroup, which forms the losses itself and saves the finishing kernel: a turn
+// takes 0.8 us, the two kernels 8.3 us at 8 experts, 9.1 at 60, 12.7 at 256 and 21.6 at 1024
+// (one with 8 turns: 9.6, 10.1, 10.7 and 20.4 us), and a launch costs the host 3.3 us.
 constexpr int kSumThreads = 1024, kSumWaves = kSumThreads / 64;
 constexpr int64_t kTokMin = 64, kOneTurns = 8;
 LossGeom loss_geom(int64_t T, int32_t E) {
-  int64_t G = T <= kOneTurns * (kSumThreads / lanes_of(E)) ? 1 : cdiv(T, kTokMin);
+  const int64_t groups = kSumThreads / lanes_of(E);
+  int64_t G = T <= kOneTurns * groups ? 1 : cdiv(T, groups > kTokMin ? groups : kTokMin);
   G = G > 512 ? 512 : G;
   LossGeom g;
   g.G = (int)G;

@@ -155,3 +155,15 @@ def test_dequantize_of_mxfp4_checks_its_tensors(monkeypatch):
     ]:
         with pytest.raises(bqm.BQMError, match=what):
             f()
+
+
+@pytest.mark.parametrize("E", [1, 8, 16, 17, 32, 33, 64, 128, 256, 1024])
+def test_router_loss_workspace_has_no_part_without_tokens(lib, E):
+    """A part of the workspace holds E sums and E counts of 4 bytes for a workgroup of the
+    first kernel; a workgroup of 1024 threads takes 1024 / lanes tokens at a time, and there
+    are no more of them than get any.  (Arrays are padded to 256 bytes.)"""
+    lanes = 4 if E <= 16 else 8 if E <= 32 else 16 if E <= 64 else 32 if E <= 128 else 64
+    for T in (1, 2049, 4096, 5000, 65536, 1 << 20):
+        parts = -(-T // (1024 // lanes))
+        most = 2 * (parts * E * 4 + 255) + 2 * (parts * 4 + 255) + 2 * 256
+        assert lib.bqm_router_loss_workspace_size(T, E) <= most, T
