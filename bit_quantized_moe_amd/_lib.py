@@ -120,9 +120,12 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        # the current stream's handle without building a Stream object (0.1 us, not 2.8 us)
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        try:
+            # the current stream's handle without building a Stream object (0.1 us, not 2.8 us)
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:      # not part of torch's public interface
+            return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -342,10 +345,13 @@ def _begin():
     if _torch is None:
         import torch
         _torch, _bf16, _f32, _i32, _u8 = torch, torch.bfloat16, torch.float32, torch.int32, torch.uint8
+    lib = load()
     try:
-        return load(), _torch._C._cuda_getDevice()
+        return lib, _torch._C._cuda_getDevice()
+    except AttributeError:          # not part of torch's public interface
+        return lib, _torch.cuda.current_device() if _torch.cuda.is_available() else -2
     except RuntimeError:
-        return load(), -2
+        return lib, -2
 
 
 def _dense(name, t, dtype, n, dev):

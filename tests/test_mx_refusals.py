@@ -167,3 +167,17 @@ def test_router_loss_workspace_has_no_part_without_tokens(lib, E):
         parts = -(-T // (1024 // lanes))
         most = 2 * (parts * E * 4 + 255) + 2 * (parts * 4 + 255) + 2 * 256
         assert lib.bqm_router_loss_workspace_size(T, E) <= most, T
+
+
+def test_binding_without_torch_s_private_calls(lib, monkeypatch):
+    """The current stream and device through torch's public interface, where the private calls
+    that the binding takes them from are not there."""
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: type("Stream", (), {"cuda_stream": 77})())
+    assert bqm._stream(None) == 77 and bqm._stream(5) == 5
+    assert bqm._begin() == (lib, 3)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: False)
+    assert bqm._begin() == (lib, -2)
