@@ -209,6 +209,46 @@ def test_dgrad_against_oracle(E, T, k, N, K, kind, gather):
     assert (host(dx)[off[E]:] == mark).all()
 
 
+# Rows of the experts: row tiles of 256 rows in every number that the largest tile's kernels
+# walk in another way (1, 2, 4 and 5 in one group; 6 = 3 + 3, 7 = 4 + 3, 9 = 5 + 4,
+# 13 = 5 + 5 + 3 in groups), whole or ending one row into a tile, and an expert without rows.
+WALK = [1025, 0, 1536, 1, 1537, 2049, 300, 3200, 1000]
+
+
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("kind,N,K", [("gemm", 1056, 256), ("gemm", 544, 736), ("gemm", 800, 224),
+                                      ("dgrad", 96, 1152), ("dgrad", 64, 640), ("dgrad", 160, 800), ("dgrad", 32, 544)])
+def test_walk_of_many_row_and_column_tiles(kind, N, K, gather):
+    """Experts of many row tiles over several column tiles, the last of them partly filled;
+    every row of an expert is written, no other is.  With the copies of whole 128-byte steps
+    (product 256 and 736, gradient 1152 and 640) and without."""
+    import torch
+    log(f"walk {kind} N={N} K={K} gather={gather}")
+    bqm = _bqm()
+    rng = np.random.default_rng([N, K, gather])
+    off = np.concatenate([[0], np.cumsum(WALK)]).astype(np.int32)
+    E, k = len(WALK), 2
+    R = int(off[E]) + 38
+    assert R % k == 0 and R >= 128 * E
+    perm = rng.permutation(R).astype(np.int32) if gather else None
+    rows, src = (perm // k, R // k) if gather else (np.arange(R), R)
+    w = bf16(rng.standard_normal((E, N, K)) * 0.05)
+    wq, wv = quantize(w), mx.dequantize_mxfp4(*mx.quantize_mxfp4(w))
+    x = bf16(rng.standard_normal((src, K if kind == "gemm" else N)))
+    mark = 7.0
+    out = torch.full((R, N if kind == "gemm" else K), mark, dtype=torch.bfloat16, device=gpu())
+    d_perm = dev(perm) if gather else None
+    if kind == "gemm":
+        bqm.bqm_mxfp4_gemm(quantize(x[None]), wq, dev(off), d_perm, k, out)
+        x = mx.dequantize_mxfp4(*mx.quantize_mxfp4(x))
+    else:
+        bqm.bqm_mxfp4_dgrad(wq, dev_bf16(x), dev(off), d_perm, k, out)
+        wv = np.ascontiguousarray(wv.transpose(0, 2, 1))
+    ref, mag = mx.product(x, wv, off, rows, np.full(out.shape, mark))
+    within(host(out), ref, 2.0 ** -8 * np.abs(ref) + x.shape[1] * 2.0 ** -23 * mag, "out")
+    assert (host(out)[off[E]:] == mark).all()
+
+
 def test_products_with_extreme_scales_and_nan_blocks():
     """Rows and columns over the whole range of scales; a NaN block reaches its own row (or
     column) only, and the experts without rows are not read."""
