@@ -509,8 +509,7 @@ __global__ void __launch_bounds__(kThreads) router_grad(const float *__restrict_
         f32x4 mult[NV] = {};
         for (int j = 0; j < k; ++j) {
           const int i = idx[t * k + j];
-          // an index from E on may name a slot that no expert has: its dw, which can be anything, counts for none
-          const float d = (unsigned)i < (unsigned)E ? dw[t * k + j] : 0.0f;
+          const float d = dw[t * k + j];
 #pragma unroll
           for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -525,7 +524,8 @@ __global__ void __launch_bounds__(kThreads) router_grad(const float *__restrict_
         for (int v = 0; v < NV; ++v)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            sa += x[v][c] * sel.a[v][c];
+            // a dropped pair's index may name a slot past E (p 0 there); its dw can be anything
+            sa += expert_of<L, NV, VEC>(v, c, l) < E ? x[v][c] * sel.a[v][c] : 0.0f;
             sm += x[v][c] * mult[v][c];
           }
         sa = group_sum<L>(sa);
