@@ -344,7 +344,8 @@ def _begin():
     global _torch, _bf16, _f32, _i32, _u8
     if _torch is None:
         import torch
-        _torch, _bf16, _f32, _i32, _u8 = torch, torch.bfloat16, torch.float32, torch.int32, torch.uint8
+        _bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+        _torch = torch      # last: another thread that finds it finds the others
     lib = load()
     try:
         return lib, _torch._C._cuda_getDevice()

@@ -1,6 +1,7 @@
 """Argument checks of the MXFP4 expert and router entry points (host only: every call here
 fails, or is empty, before anything is launched)."""
 import ctypes as C
+import sys
 
 import pytest
 
@@ -181,3 +182,28 @@ def test_binding_without_torch_s_private_calls(lib, monkeypatch):
     assert bqm._begin() == (lib, 3)
     monkeypatch.setattr(torch.cuda, "is_available", lambda: False)
     assert bqm._begin() == (lib, -2)
+
+
+def test_first_calls_of_two_threads_at_once(lib, monkeypatch):
+    """Wherever another thread's first call comes between two instructions of this one's, it
+    finds the types that its checks compare with, or sets them itself."""
+    names = ("_bf16", "_f32", "_i32", "_u8")
+    for name in ("_torch", *names):
+        monkeypatch.setattr(bqm, name, None)
+    half = []
+
+    def trace(frame, event, arg):
+        if frame.f_code is not bqm._begin.__code__:
+            return None
+        frame.f_trace_opcodes = True
+        if bqm._torch is not None and any(getattr(bqm, n) is None for n in names):
+            half.append(frame.f_lasti)
+        return trace
+
+    before = sys.gettrace()
+    sys.settrace(trace)
+    try:
+        bqm._begin()
+    finally:
+        sys.settrace(before)
+    assert bqm._torch is torch and not half
