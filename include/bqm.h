@@ -172,7 +172,9 @@ bqm_status bqm_quantize_mxfp4(const uint16_t *x, bqm_qtensor *out /* host struct
  * nf4moe page, section "The fix: dequant-on-forward for routed experts", for NF4):
  *   NVFP4: bf16_rne(fl32(e2m1(code) * e4m3(scale)) * s_dec)  (one FP32 rounding)
  *   NF4:   bf16_rne(fl32(level[code] * absmax)), absmax' when nested
- *   MXFP4: e2m1(code) * 2^(scale - 127), exact in bf16; NaN for scale code 255
+ *   MXFP4: e2m1(code) * 2^(scale - 127), exact in bf16 for the scales that
+ *   bqm_quantize_mxfp4 writes (at most 252); codes of other origin overflow to infinity
+ *   from 2^128 on (4 and 6 with scale code 253, 2 and more with 254); NaN for code 255
  * q: a stack as bqm_quantize_nvfp4 / bqm_quantize_nf4 / bqm_nf4_nest /
  * bqm_quantize_mxfp4 wrote it
  * (read only); y: bf16 [n_mat, rows, cols], written.  Errors: a bad format, a
@@ -212,9 +214,11 @@ bqm_status bqm_permute(const int32_t *topk_idx, int64_t T, int32_t E, int32_t k,
  * as bqm_permute gives them.  One layer, forward and backward:
  *   bqm_route, bqm_permute, bqm_router_loss; bqm_quantize_mxfp4 (x);
  *   bqm_mxfp4_gemm (x, w_gu, perm) -> h; bqm_swiglu_ckpt_fwd (h) -> checkpoint, a in
- *   MXFP4; bqm_mxfp4_gemm (a, w_dn, no perm) -> the routed rows y, combined per token;
+ *   MXFP4; bqm_mxfp4_gemm (a, w_dn, no perm) -> the routed rows y;
  *   bqm_mxfp4_dgrad (w_dn, dy, perm) -> da; bqm_swiglu_ckpt_bwd -> dh, dtopk_w;
  *   bqm_mxfp4_dgrad (w_gu, dh, no perm) -> the rows of dx; bqm_router_grad -> dlogits.
+ * A token's output (sum over j of topk_w y[inv]) and its dx (the sum of its rows) are the
+ * caller's to add up; rows of dropped pairs hold what the buffer held before.
  * The activation quantizers are the identity in the backward, as in the layer below. */
 
 /* Grouped product y[pos, n] = sum_k X[row, k] W[e, n, k], rounded to bf16 once, for
@@ -233,13 +237,16 @@ bqm_status bqm_mxfp4_gemm(const bqm_qtensor *x /* host struct */, const bqm_qten
 
 /* Its input gradient dx[pos, k] = sum_n dY[row, n] DQ(W)[e, n, k] over the same rowwise
  * copy: dy bf16 [dy_rows, N], dx bf16 [R, K]; the rest as for bqm_mxfp4_gemm (R =
- * dy_rows * k with perm, dy_rows without).  dY is not quantized; sums are FP32. */
+ * dy_rows * k with perm, dy_rows without).  dY is not quantized; sums are FP32.  DQ(W) is
+ * what bqm_dequantize gives: a weight of other origin that overflows bf16 there is infinite
+ * here, while bqm_mxfp4_gemm multiplies its value. */
 bqm_status bqm_mxfp4_dgrad(const bqm_qtensor *w /* host struct */, const uint16_t *dy, int64_t dy_rows,
                            const int32_t *offsets, const int32_t *perm, int32_t k, int64_t R, uint16_t *dx,
                            void *stream);
 
-/* SwiGLU a = silu(g) u of h = [g, u] (bf16 [R, 2I], I % 32 == 0), computed in FP32, and
- * an 8-bit copy of h for the backward: h8 uint8 [R, 2I] E4M3FN bits, h8_scales uint8
+/* SwiGLU a = silu(g) u of h = [g, u] (bf16 [R, 2I], I % 32 == 0), computed in FP32 (silu
+ * is 0 below g = -88, where it is under 10^-35 in size), and an 8-bit copy of h for the
+ * backward: h8 uint8 [R, 2I] E4M3FN bits, h8_scales uint8
  * [R, 2I/32] E8M0 codes, per 32-block the smallest 2^s with max|h| 2^-s <= 448 (no value
  * saturates; each is off by at most 2^-4 of itself or 2^-10 2^s).  A block with an
  * infinity or NaN gets scale code 255 and reads back as NaN.
@@ -272,7 +279,8 @@ bqm_status bqm_swiglu_ckpt_bwd(const uint8_t *h8, const uint8_t *h8_scales, cons
  * logit has p = 0 and logsumexp 0.  A NaN logit of a token that counts makes both losses
  * NaN.  Logits of tokens that do not count may hold anything.
  * logits f32 [T, E], topk_idx i32 [T, k]; limits as for bqm_route, T * k < 2^31.  Sums of
- * p are FP32 per workgroup and FP64 across, in a fixed order.  ws:
+ * p and of logsumexp^2 are FP32 per workgroup (of which there are up to 512) and FP64
+ * across, in a fixed order.  ws:
  * bqm_router_loss_workspace_size() bytes; calls that share one must not overlap. */
 size_t bqm_router_loss_workspace_size(int64_t T, int32_t E);
 bqm_status bqm_router_loss(const float *logits, const int32_t *topk_idx, const uint8_t *valid, int64_t T, int32_t E,

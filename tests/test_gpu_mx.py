@@ -281,6 +281,37 @@ def test_products_with_extreme_scales_and_nan_blocks():
     within(host(dx), ref, 2.0 ** -8 * np.abs(ref) + N * 2.0 ** -23 * mag, "dx")
 
 
+@pytest.mark.parametrize("K", [256, 96])
+def test_products_with_scales_past_bf16(K):
+    """A weight row with the two largest scale codes, whose values reach 6 2^127: the product
+    multiplies the values, the gradient what the dequantizer gives (infinity from 2^128 on)."""
+    import torch
+    log(f"mxfp4 products, scale codes 253 and 254, K={K}")
+    bqm = _bqm()
+    rng = np.random.default_rng(K)
+    N = 64
+    w = quantize(bf16(rng.standard_normal((1, N, K))))
+    w.codes[0, 3].copy_(dev(rng.integers(0, 256, K // 2).astype(np.uint8)))
+    w.scales[0, 3].copy_(dev(np.where(np.arange(K // 32) % 2, 254, 253).astype(np.uint8)))
+    x = bf16(rng.standard_normal((5, K)) * 2.0 ** -40)
+    off = dev(np.array([0, 5], np.int32))
+    y = torch.empty((5, N), dtype=torch.bfloat16, device=gpu())
+    bqm.bqm_mxfp4_gemm(quantize(x[None]), w, off, None, 1, y)
+    ref, mag = mx.product(mx.dequantize_mxfp4(*mx.quantize_mxfp4(x)), mx.dequantize_mxfp4(host(w.codes), host(w.scales)),
+                          [0, 5], np.arange(5), np.zeros((5, N)))
+    within(host(y), ref, 2.0 ** -8 * np.abs(ref) + K * 2.0 ** -23 * mag, "y")
+    dy = np.zeros((5, N))
+    dy[:, 3] = [1, -1, 0.5, 2.0 ** -9, -2.0]
+    dx, dq = (torch.empty(s, dtype=torch.bfloat16, device=gpu()) for s in ((5, K), (1, N, K)))
+    bqm.bqm_mxfp4_dgrad(w, dev_bf16(dy), off, None, 1, dx)
+    bqm.bqm_dequantize(w, dq)
+    wv = host(dq)[0, 3]
+    assert np.isinf(wv).any() and not np.isinf(wv).all()
+    with np.errstate(over="ignore"):        # -2 times 2^127 and more is past bf16 as well
+        want = bf16(dy[:, 3:4] * wv)
+    assert np.array_equal(host(dx), want)
+
+
 def test_products_past_four_gigabytes_of_weights():
     import torch
     log("mxfp4 products, expert stack over 4 GiB")
