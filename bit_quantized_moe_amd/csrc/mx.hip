@@ -780,11 +780,16 @@ __global__ void __launch_bounds__(NTHR, OCC) mx_tiles(MxParams p) {
   // each XCD (workgroups b % 8) walks a contiguous range of tiles, so that the tiles in
   // flight there share an expert's rows and weights in its L2.  In the largest tile's kernels
   // an expert's row tiles are walked in groups of about GM, column tile by column tile: the 32
-  // tiles that an XCD has in flight are then 4 x 8 and not 2 x 16 of them (64 experts of 1024
-  // rows, 4096 x 6144: product reads 1.96 -> 1.30 GB and takes 958 -> 940 us, gradient 3.43 ->
-  // 2.56 GB, 2521 -> 2478 us; 2 or 8 row tiles gain less, and the smaller tiles lose 1%).  The
-  // groups are even and end with the expert: groups of four across experts made the product
-  // of 64 experts of 950 to 1100 rows read 2.7 GB, not 1.9, in 1069 us, not 1009.
+  // tiles that an XCD has in flight are then 4 x 8 and not 2 x 16 of them.  The groups are
+  // even and end with the expert.  64 experts, 4096 x 6144, GB read and us, three kernels in
+  // turn on one card (2 or 8 row tiles gain less, and the smaller tiles lose 1%):
+  //                                 product          gradient
+  //   1024 rows each, no groups     1.96   926       3.41  2534
+  //     groups of 4 or about 4      1.30   904       2.56  2554
+  //   922 to 1096 rows, no groups   3.23  1003       4.83  2788
+  //     groups of 4 over experts    2.76  1004       5.21  2867
+  //     even groups per expert      1.96   930       4.75  2797
+  // (The gradient is bound by the matrix unit and keeps its time.)
   constexpr int GM = TM == 4 ? 4 : 1;
   const int per = (total + 7) / 8;
   const int first = (blockIdx.x & 7) * per, last = min(first + per, total);
@@ -882,13 +887,36 @@ constexpr int kCUs = 256;
 
 // The tile goes by the rows an expert has on average (the host knows R and E, not the
 // offsets), one tile of rows as long as it can hold them: every further one reads the
-// expert's weights again, and a tile's empty rows cost what full ones do.  Measured at
-// N = 2816, K = 2048, 60 experts (gradient N = 2048, 64 experts), us at the given rows:
-//   product   rows  1   16   32   60  100  160  256   gradient  rows 12   32   64  100  256
-//   32 x 128       41   43   47   60                  32 x 256       48   49   96   90
-//   64 x 128       42   45   48   54   68   91  119   64 x 256       56   58   64   95  227
-//   128 x 128      43   46   50   55   63   83   97
-//   256 x 256      52   54   56   61   68   77   94   256 x 256      72   72   74   81  132
+// expert's weights again, and a tile's empty rows cost what full ones do.  Pairs that belong
+// to no expert count as rows, and experts without rows as experts.  Measured in us, product
+// N = 2816, K = 2048, 60 experts, gradient N = K = 2048, 64 experts; e: the same rows for
+// every expert, r: every row's expert at random, s: with weights 1, 2^-0.7, 3^-0.7, ...
+//   product     rows 12   24   28   32   40   56   64   96  128  160  256
+//   32 x 128  e      39   40   41   41   49   51   50   65   83   98  149
+//             r      38   40   41   43   49   52   58   73   87  106  158
+//             s      38   43   47   46   49   57   61   77   91  108  162
+//   64 x 128  e      41   42   43   43   43   45   45   63   66   86  112
+//             r      41   42   42   43   43   45   53   63   74   86  125
+//             s      41   42   42   43   50   52   53   63   79   90  129
+//   128 x 128 e      42   43   44   44   45   46   47   54   58   74   86
+//             r      42   43   43   44   44   46   49   55   63   75   98
+//             s      43   46   46   48   47   50   50   58   65   73   98
+//   256 x 256 e      50   50   51   51   51   52   52   58   59   67   82
+//             r      50   50   50   51   51   53   54   58   62   68  104
+//             s      50   52   53   54   55   61   59   63   65   82   88
+//   gradient    rows 12   24   28   32   40   56   64   72   88  112  160
+//   32 x 256  e      43   44   44   44   84   86   86  133  130  171  222
+//             r      44   43   62   62   85  106  104  124  152  185  229
+//             s      60   61   61   62   81  102  102  122  143  164  225
+//   64 x 256  e      51   51   51   51   52   54   54  104  104  104  162
+//             r      51   51   51   52   53   77   78  100  104  125  153
+//             s      73   73   74   74   75   77   78   98  101  124  152
+//   256 x 256 e      69   69   69   68   69   71   71   76   76   79   97
+//             r      69   68   68   68   69   72   73   73   76   81   94
+//             s      68   73   82  109  112  119  134  134  137  138  142
+// The 32-row tile ends at 24 rows and not at the 32 that it can hold: with uneven rows some
+// expert has more from about 28 on.  The gradient's 64-row tile ends between where it loses
+// at random (about 56) and where it does with popular experts (above 112).
 // Without FAST there are the middle and the largest tile.
 constexpr int64_t kRows32 = 24, kRows64 = 64, kRows128 = 128, kRowsDgrad64 = 88;
 
