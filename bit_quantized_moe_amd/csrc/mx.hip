@@ -109,11 +109,14 @@ constexpr int PER = kMaxE / NTHR;
 struct TileMap {
   int first[PER + 1];  // row tiles before expert PER tid + i
 
-  // returns the number of row tiles
+  // returns the number of row tiles, at most as many as offsets that do not fall can make:
+  // falling ones give rows to many experts, and the tiles of all of them (E / 2 times R rows)
+  // need not fit 32 bits, so the sums are unsigned and tiles past that number are left out
   template <int BM>
   __device__ int build(const MxParams &p, int *wsum) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int c[PER], run = 0;
+    int c[PER];
+    uint32_t run = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int e = tid * PER + i;
@@ -122,24 +125,26 @@ struct TileMap {
       c[i] = n > 0 ? (n + BM - 1) / BM : 0;
       run += c[i];
     }
-    int inc = run;
+    uint32_t inc = run;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const int t = __shfl_up(inc, o, 64);
+      const uint32_t t = __shfl_up(inc, o, 64);
       if (lane >= o) inc += t;
     }
-    if (lane == 63) wsum[wave] = inc;
+    if (lane == 63) wsum[wave] = (int)inc;
     __syncthreads();
-    int base = 0, total = 0;
+    uint32_t base = 0, total = 0;
 #pragma unroll
     for (int q = 0; q < NTHR / 64; ++q) {
-      if (q < wave) base += wsum[q];
-      total += wsum[q];
+      if (q < wave) base += (uint32_t)wsum[q];
+      total += (uint32_t)wsum[q];
     }
-    first[0] = base + inc - run;
+    base += inc - run;
+    first[0] = (int)base;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) first[i + 1] = first[i] + c[i];
-    return total;
+    for (int i = 0; i < PER; ++i) first[i + 1] = (int)(base += c[i]);
+    const int64_t most = p.R / BM + (p.E < p.R ? p.E : p.R);
+    return (int)min((int64_t)total, most);
   }
 
   // the owner of row tile mt writes its expert, that expert's first tile and number of tiles to found

@@ -228,7 +228,8 @@ bqm_status bqm_permute(const int32_t *topk_idx, int64_t T, int32_t E, int32_t k,
  * then not read); y bf16 [R, N].  The products of the 4-bit values are exact, sums are
  * FP32.  Rows that belong to no expert (from offsets[E] on) are left as they were; only
  * experts with rows are read.  Offsets are clamped to [0, R] and source rows to [0, rows)
- * where they are read, so that no value in them reaches memory outside the tensors.
+ * where they are read, so that no value in them reaches memory outside the tensors; a row
+ * that offsets which fall give to several experts gets one's result or another's, or none.
  * Results do not depend on the other rows of the batch beyond the order of the FP32
  * sums, which goes by R / E. */
 bqm_status bqm_mxfp4_gemm(const bqm_qtensor *x /* host struct */, const bqm_qtensor *w /* host struct */,

@@ -312,6 +312,53 @@ def test_products_with_scales_past_bf16(K):
     assert np.array_equal(host(dx), want)
 
 
+@pytest.mark.parametrize("kind,N,K", [("gemm", 96, 256), ("gemm", 160, 96), ("dgrad", 64, 256), ("dgrad", 96, 160)])
+@pytest.mark.parametrize("R", [64, 1500])
+def test_offsets_and_rows_out_of_range_are_clamped(kind, N, K, R):
+    """Offsets below 0, past R and falling, and source rows of no token: a result is the row's
+    expert's product of the clamped source row, that of any of its experts where offsets that
+    fall give it to several, and what it was where they give it to none."""
+    import torch
+    log(f"clamped {kind} N={N} K={K} R={R}")
+    bqm = _bqm()
+    rng = np.random.default_rng([N, K, R])
+    k = 2
+    off = np.array([5, R // 4, R // 4 + 3, R // 8, R // 2, R // 2, 3 * R // 4, R // 2 + 5, (1 << 31) - 1, -7, 3,
+                    -(1 << 31)], np.int32)
+    E = len(off) - 1
+    perm = rng.integers(0, R, R).astype(np.int32)
+    wild = rng.random(R) < 0.2
+    perm[wild] = np.array([-1, -9, R, R + 5, (1 << 31) - 1, -(1 << 31)])[rng.integers(0, 6, wild.sum())]
+    src = R // k
+    rows = np.clip(np.trunc(perm / k).astype(np.int64), 0, src - 1)
+    w = bf16(rng.standard_normal((E, N, K)) * 0.05)
+    wq, wv = quantize(w), mx.dequantize_mxfp4(*mx.quantize_mxfp4(w))
+    x = bf16(rng.standard_normal((src, K if kind == "gemm" else N)))
+    mark = 7.0
+    # rows of the mark on both sides of the output, too
+    whole = torch.full((R + 512, N if kind == "gemm" else K), mark, dtype=torch.bfloat16, device=gpu())
+    out = whole[256:256 + R]
+    if kind == "gemm":
+        bqm.bqm_mxfp4_gemm(quantize(x[None]), wq, dev(off), dev(perm), k, out)
+        x = mx.dequantize_mxfp4(*mx.quantize_mxfp4(x))
+    else:
+        bqm.bqm_mxfp4_dgrad(wq, dev_bf16(x), dev(off), dev(perm), k, out)
+        wv = np.ascontiguousarray(wv.transpose(0, 2, 1))
+    got, at = host(whole), np.clip(off.astype(np.int64), 0, R)
+    assert (got[:256] == mark).all() and (got[256 + R:] == mark).all()
+    got, owners = got[256:256 + R], np.zeros(R, int)
+    found = np.zeros(got.shape, bool)
+    for e in range(E):
+        a, b = at[e], at[e + 1]
+        if b <= a:
+            continue
+        ref, mag = x[rows[a:b]] @ wv[e].T, np.abs(x[rows[a:b]]) @ np.abs(wv[e]).T
+        found[a:b] |= np.abs(got[a:b] - ref) <= 2.0 ** -8 * np.abs(ref) + x.shape[1] * 2.0 ** -23 * mag
+        owners[a:b] += 1
+    assert (owners == 0).any() and (owners == 1).any() and (owners > 1).any()
+    assert found[owners > 0].all() and (got[owners == 0] == mark).all()
+
+
 def test_products_past_four_gigabytes_of_weights():
     import torch
     log("mxfp4 products, expert stack over 4 GiB")
