@@ -12,6 +12,7 @@ from ._lib import (BQMError, FMT_MXFP4, FMT_NF4, FMT_NVFP4, MoEDesc, QTensor, SC
                    bqm_quantize_nvfp4_workspace_size,
                    bqm_mxfp4_dgrad, bqm_mxfp4_gemm, bqm_quantize_mxfp4, bqm_router_grad, bqm_router_loss,
                    bqm_router_loss_workspace_size, bqm_swiglu_ckpt_bwd, bqm_swiglu_ckpt_fwd,
+                   bqm_combine, bqm_combine_grad, bqm_dispatch,
                    bqm_route, load, nf4_nest_groups, quantize_stack)
 
 __all__ = [n for n in dir() if n.startswith("bqm_")] + [

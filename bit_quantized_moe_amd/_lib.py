@@ -34,7 +34,8 @@ EXPORTS = ["bqm_abi_version", "bqm_last_error", "bqm_quantize_nvfp4_workspace_si
            "bqm_permute_workspace_size", "bqm_permute", "bqm_moe_workspace_size", "bqm_moe_fwd",
            "bqm_moe_dgrad", "bqm_moe_dgrad_colwise", "bqm_lora_grad", "bqm_nf4_nest", "bqm_quantize_mxfp4",
            "bqm_mxfp4_gemm", "bqm_mxfp4_dgrad", "bqm_swiglu_ckpt_fwd", "bqm_swiglu_ckpt_bwd",
-           "bqm_router_loss_workspace_size", "bqm_router_loss", "bqm_router_grad"]
+           "bqm_router_loss_workspace_size", "bqm_router_loss", "bqm_router_grad", "bqm_dispatch", "bqm_combine",
+           "bqm_combine_grad"]
 
 
 class BQMError(RuntimeError):
@@ -99,6 +100,9 @@ def load(path: str = LIB_PATH):
         "bqm_router_loss_workspace_size": (sz, [i64, i32]),
         "bqm_router_loss": (C.c_int, [vp, vp, vp, i64, i32, i32, vp, vp, vp, sz, vp]),
         "bqm_router_grad": (C.c_int, [vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, vp, vp]),
+        "bqm_dispatch": (C.c_int, [vp, vp, i64, i64, i32, vp, vp, vp]),
+        "bqm_combine": (C.c_int, [vp, vp, vp, vp, i64, i64, i32, vp, vp, vp]),
+        "bqm_combine_grad": (C.c_int, [vp, vp, vp, vp, i64, i64, i32, vp, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -332,9 +336,9 @@ def bqm_lora_grad(d: MoEDesc, x, dy, ws, dA_gu, dB_gu, dA_dn, dB_dn, stream=None
 
 
 # ----------------------------------------------------------------------------
-# experts over MXFP4 and the router's training.  These calls take their sizes from the
-# tensors, so the tensors' types, shapes and layout are checked here; everything else is
-# checked behind the C ABI.
+# experts over MXFP4, the router's training, rows between token and expert order.  These
+# calls take their sizes from the tensors, so the tensors' types, shapes and layout are
+# checked here; everything else is checked behind the C ABI.
 # ----------------------------------------------------------------------------
 _torch = _bf16 = _f32 = _i32 = _u8 = None
 
@@ -461,3 +465,50 @@ def bqm_router_grad(logits, topk_idx, valid, counts, dtopk_w, dloss, renorm, dlo
                                _dense("dtopk_w", dtopk_w, _f32, T * k, dev), _dense("dloss", dloss, _f32, 2, dev), T, E, k,
                                int(renorm), _dense("dlogits", dlogits, _f32, T * E, dev), _stream(stream)))
     return dlogits
+
+
+def _pairs(name, rows, T):
+    """Pairs per token of a tensor [T * k, H] (or inv [T, k], flattened or not)."""
+    if T and rows and rows % T == 0:
+        return rows // T
+    if T == 0 and rows == 0:
+        return 1
+    raise BQMError(-2, f"{name}: {rows} pairs for {T} tokens")
+
+
+def bqm_dispatch(x, inv, rows, n_rows=None, stream=None):
+    """rows [R, H]: x [T, H] at the place inv [T, k] of each pair.  n_rows: a one-element int32
+    tensor (offsets[E:], say); pairs whose place lies behind it are dropped."""
+    lib, dev = _begin()
+    T, H = x.shape
+    R = inv.numel()
+    k = _pairs("inv", R, T)
+    _check(lib.bqm_dispatch(_dense("x", x, _bf16, T * H, dev), _dense("inv", inv, _i32, R, dev), T, H, k,
+                            _dense("n_rows", n_rows, _i32, 1, dev), _dense("rows", rows, _bf16, R * H, dev),
+                            _stream(stream)))
+    return rows
+
+
+def bqm_combine(y, inv, out, topk_w=None, residual=None, n_rows=None, stream=None):
+    """out [T, H]: each token's rows of y [R, H] times topk_w [T, k] (None: 1), plus residual."""
+    lib, dev = _begin()
+    T, H = out.shape
+    R = inv.numel()
+    k = _pairs("inv", R, T)
+    _check(lib.bqm_combine(_dense("y", y, _bf16, R * H, dev), _dense("inv", inv, _i32, R, dev),
+                           _dense("topk_w", topk_w, _f32, R, dev), _dense("residual", residual, _bf16, T * H, dev), T, H,
+                           k, _dense("n_rows", n_rows, _i32, 1, dev), _dense("out", out, _bf16, T * H, dev),
+                           _stream(stream)))
+    return out
+
+
+def bqm_combine_grad(dout, inv, y=None, topk_w=None, dy=None, dtopk_w=None, n_rows=None, stream=None):
+    """dout [T, H] -> dy [R, H] and dtopk_w [T, k] (which needs y [R, H]), where given."""
+    lib, dev = _begin()
+    T, H = dout.shape
+    R = inv.numel()
+    k = _pairs("inv", R, T)
+    _check(lib.bqm_combine_grad(_dense("dout", dout, _bf16, T * H, dev), _dense("y", y, _bf16, R * H, dev),
+                                _dense("inv", inv, _i32, R, dev), _dense("topk_w", topk_w, _f32, R, dev), T, H, k,
+                                _dense("n_rows", n_rows, _i32, 1, dev), _dense("dy", dy, _bf16, R * H, dev),
+                                _dense("dtopk_w", dtopk_w, _f32, R, dev), _stream(stream)))

@@ -217,8 +217,9 @@ bqm_status bqm_permute(const int32_t *topk_idx, int64_t T, int32_t E, int32_t k,
  *   MXFP4; bqm_mxfp4_gemm (a, w_dn, no perm) -> the routed rows y;
  *   bqm_mxfp4_dgrad (w_dn, dy, perm) -> da; bqm_swiglu_ckpt_bwd -> dh, dtopk_w;
  *   bqm_mxfp4_dgrad (w_gu, dh, no perm) -> the rows of dx; bqm_router_grad -> dlogits.
- * A token's output (sum over j of topk_w y[inv]) and its dx (the sum of its rows) are the
- * caller's to add up; rows of dropped pairs hold what the buffer held before.
+ * A token's output (sum over j of topk_w y[inv]) and its dx (the sum of its rows) are
+ * bqm_combine's, with and without topk_w; rows of dropped pairs hold what the buffer held
+ * before.
  * The activation quantizers are the identity in the backward, as in the layer below. */
 
 /* Grouped product y[pos, n] = sum_k X[row, k] W[e, n, k], rounded to bf16 once, for
@@ -296,6 +297,34 @@ bqm_status bqm_router_loss(const float *logits, const int32_t *topk_idx, const u
 bqm_status bqm_router_grad(const float *logits, const int32_t *topk_idx, const uint8_t *valid, const int32_t *counts,
                            const float *dtopk_w, const float *dloss, int64_t T, int32_t E, int32_t k, int32_t renorm,
                            float *dlogits, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Rows between token order and expert order.  T tokens of H bf16 elements, k pairs each;
+ * pair f = t * k + j of token t stands at row inv[f] (i32 [T, k], as bqm_permute gives it) of
+ * the expert-ordered tensors [R, H], R = T * k.  Pairs with inv[f] < 0 or inv[f] >= n are
+ * dropped: n = *n_rows (device int32, for instance offsets + E; 4-byte aligned), at most R,
+ * or R where n_rows is NULL.  Nothing is read or written for a dropped pair, and the rows that
+ * no pair stands at are left as they were.  Two pairs at one row get one's result or the
+ * other's.  1 <= H < 2^24 (16-byte accesses where 8 divides H), k >= 1, T * k < 2^31; T == 0
+ * is a no-op.  topk_w f32 [T, k], NULL: 1.  Sums are FP32 in the order of j. */
+
+/* rows[inv[f]] = x[t]: a token's row at the place of each of its pairs, as the experts'
+ * products without perm, or an exchange between devices, read them.  Its gradient is
+ * bqm_combine without topk_w. */
+bqm_status bqm_dispatch(const uint16_t *x, const int32_t *inv, int64_t T, int64_t H, int32_t k, const int32_t *n_rows,
+                        uint16_t *rows, void *stream);
+
+/* out[t] = sum_j topk_w[f] y[inv[f]] + residual[t], rounded to bf16 once: a token's output
+ * from its experts' rows y [R, H], added to residual (bf16 [T, H] or NULL; may be out). */
+bqm_status bqm_combine(const uint16_t *y, const int32_t *inv, const float *topk_w, const uint16_t *residual, int64_t T,
+                       int64_t H, int32_t k, const int32_t *n_rows, uint16_t *out, void *stream);
+
+/* Its gradient, dout bf16 [T, H] (which is also the residual's):
+ *   dy[inv[f]] = topk_w[f] dout[t]      -> bf16 [R, H], or NULL; may be y
+ *   dtopk_w[f] = <dout[t], y[inv[f]]>   -> f32 [T, k], or NULL (y is then not read); 0 for
+ *                                          dropped pairs */
+bqm_status bqm_combine_grad(const uint16_t *dout, const uint16_t *y, const int32_t *inv, const float *topk_w, int64_t T,
+                            int64_t H, int32_t k, const int32_t *n_rows, uint16_t *dy, float *dtopk_w, void *stream);
 
 /* ---------------------------------------------------------------------------
  * The MoE layer.  Expert weights are stacks w_gu [E, 2I, H] (gate rows 0..I-1,
