@@ -12,9 +12,10 @@ from ._lib import (BQMError, FMT_MXFP4, FMT_NF4, FMT_NVFP4, MoEDesc, QTensor, SC
                    bqm_quantize_nvfp4_workspace_size,
                    bqm_mxfp4_dgrad, bqm_mxfp4_gemm, bqm_quantize_mxfp4, bqm_router_grad, bqm_router_loss,
                    bqm_router_loss_workspace_size, bqm_swiglu_ckpt_bwd, bqm_swiglu_ckpt_fwd,
-                   bqm_combine, bqm_combine_grad, bqm_dispatch,
+                   ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, bqm_act_grad, bqm_combine, bqm_combine_grad, bqm_dispatch,
+                   bqm_linear_dgrad, bqm_linear_fwd, bqm_linear_wgrad, bqm_linear_workspace_size,
                    bqm_route, load, nf4_nest_groups, quantize_stack)
 
 __all__ = [n for n in dir() if n.startswith("bqm_")] + [
-    "BQMError", "FMT_MXFP4", "FMT_NF4", "FMT_NVFP4", "MoEDesc", "QTensor", "SCALE_PER_ROW", "SCALE_PER_TENSOR", "STAGES", "STAGE_COUNT",
+    "ACT_GELU_TANH", "ACT_NONE", "ACT_RELU", "ACT_SILU", "BQMError", "FMT_MXFP4", "FMT_NF4", "FMT_NVFP4", "MoEDesc", "QTensor", "SCALE_PER_ROW", "SCALE_PER_TENSOR", "STAGES", "STAGE_COUNT",
     "alloc_qtensor", "load", "nf4_nest_groups", "quantize_stack"]

@@ -20,6 +20,10 @@ FMT_NF4 = 2
 FMT_MXFP4 = 3
 SCALE_PER_TENSOR = 0
 SCALE_PER_ROW = 1
+ACT_NONE = 0
+ACT_RELU = 1
+ACT_SILU = 2
+ACT_GELU_TANH = 3
 
 STAGES = ["permute", "act_quant_x", "lora_a_gu", "gate_up_fwd", "act_quant_a", "lora_a_dn", "down_fwd",
           "combine_fwd", "dtopk", "lora_b_dn", "down_dgrad", "lora_b_gu", "gate_up_dgrad", "combine_dgrad",
@@ -35,7 +39,8 @@ EXPORTS = ["bqm_abi_version", "bqm_last_error", "bqm_quantize_nvfp4_workspace_si
            "bqm_moe_dgrad", "bqm_moe_dgrad_colwise", "bqm_lora_grad", "bqm_nf4_nest", "bqm_quantize_mxfp4",
            "bqm_mxfp4_gemm", "bqm_mxfp4_dgrad", "bqm_swiglu_ckpt_fwd", "bqm_swiglu_ckpt_bwd",
            "bqm_router_loss_workspace_size", "bqm_router_loss", "bqm_router_grad", "bqm_dispatch", "bqm_combine",
-           "bqm_combine_grad"]
+           "bqm_combine_grad", "bqm_linear_workspace_size", "bqm_linear_fwd", "bqm_linear_dgrad", "bqm_linear_wgrad",
+           "bqm_act_grad"]
 
 
 class BQMError(RuntimeError):
@@ -103,6 +108,11 @@ def load(path: str = LIB_PATH):
         "bqm_dispatch": (C.c_int, [vp, vp, i64, i64, i32, vp, vp, vp]),
         "bqm_combine": (C.c_int, [vp, vp, vp, vp, i64, i64, i32, vp, vp, vp]),
         "bqm_combine_grad": (C.c_int, [vp, vp, vp, vp, i64, i64, i32, vp, vp, vp, vp]),
+        "bqm_linear_workspace_size": (sz, [i64, i64, i64]),
+        "bqm_linear_fwd": (C.c_int, [vp, vp, vp, i32, vp, i64, i64, i64, vp, vp, vp, sz, vp]),
+        "bqm_linear_dgrad": (C.c_int, [vp, vp, vp, i32, vp, i64, i64, i64, vp, vp, sz, vp]),
+        "bqm_linear_wgrad": (C.c_int, [vp, vp, i32, i64, i64, i64, vp, vp, vp, sz, vp]),
+        "bqm_act_grad": (C.c_int, [vp, vp, i32, i64, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -336,9 +346,9 @@ def bqm_lora_grad(d: MoEDesc, x, dy, ws, dA_gu, dB_gu, dA_dn, dB_dn, stream=None
 
 
 # ----------------------------------------------------------------------------
-# experts over MXFP4, the router's training, rows between token and expert order.  These
-# calls take their sizes from the tensors, so the tensors' types, shapes and layout are
-# checked here; everything else is checked behind the C ABI.
+# experts over MXFP4, the router's training, rows between token and expert order, the dense
+# product.  These calls take their sizes from the tensors, so the tensors' types, shapes and
+# layout are checked here; everything else is checked behind the C ABI.
 # ----------------------------------------------------------------------------
 _torch = _bf16 = _f32 = _i32 = _u8 = None
 
@@ -512,3 +522,53 @@ def bqm_combine_grad(dout, inv, y=None, topk_w=None, dy=None, dtopk_w=None, n_ro
                                 _dense("inv", inv, _i32, R, dev), _dense("topk_w", topk_w, _f32, R, dev), T, H, k,
                                 _dense("n_rows", n_rows, _i32, 1, dev), _dense("dy", dy, _bf16, R * H, dev),
                                 _dense("dtopk_w", dtopk_w, _f32, R, dev), _stream(stream)))
+
+
+def bqm_linear_workspace_size(M, N, K) -> int:
+    return load().bqm_linear_workspace_size(M, N, K)
+
+
+def bqm_linear_fwd(x, w, y, bias=None, act=ACT_NONE, residual=None, z=None, ws=None, stream=None):
+    """y [M, N] = act(x [M, K] w [N, K]^T + bias [N]) + residual [M, N]; z [M, N]: the
+    pre-activation, where given.  ws: uint8, bqm_linear_workspace_size(M, N, K)."""
+    lib, dev = _begin()
+    (M, K), N = x.shape, w.shape[0]
+    wsb = 0 if ws is None else ws.numel()
+    _check(lib.bqm_linear_fwd(_dense("x", x, _bf16, M * K, dev), _dense("w", w, _bf16, N * K, dev),
+                              _dense("bias", bias, _bf16, N, dev), act, _dense("residual", residual, _bf16, M * N, dev), M,
+                              N, K, _dense("y", y, _bf16, M * N, dev), _dense("z", z, _bf16, M * N, dev),
+                              _dense("ws", ws, _u8, wsb, dev), wsb, _stream(stream)))
+    return y
+
+
+def bqm_linear_dgrad(dz, w, dx, zx=None, act=ACT_NONE, add=None, ws=None, stream=None):
+    """dx [M, K] = dz [M, N] w [N, K], times act'(zx [M, K]) with an activation, plus add [M, K]."""
+    lib, dev = _begin()
+    (N, K), M = w.shape, dz.shape[0]
+    wsb = 0 if ws is None else ws.numel()
+    _check(lib.bqm_linear_dgrad(_dense("dz", dz, _bf16, M * N, dev), _dense("w", w, _bf16, N * K, dev),
+                                _dense("zx", zx, _bf16, M * K, dev), act, _dense("add", add, _bf16, M * K, dev), M, N, K,
+                                _dense("dx", dx, _bf16, M * K, dev), _dense("ws", ws, _u8, wsb, dev), wsb,
+                                _stream(stream)))
+    return dx
+
+
+def bqm_linear_wgrad(dz, x, dw, dbias=None, accumulate=False, ws=None, stream=None):
+    """dw float32 [N, K] = dz [M, N]^T x [M, K], dbias float32 [N] = the sum of dz's rows; added
+    to what they hold with accumulate."""
+    lib, dev = _begin()
+    (M, N), K = dz.shape, x.shape[1]
+    wsb = 0 if ws is None else ws.numel()
+    _check(lib.bqm_linear_wgrad(_dense("dz", dz, _bf16, M * N, dev), _dense("x", x, _bf16, M * K, dev), int(accumulate), M,
+                                N, K, _dense("dw", dw, _f32, N * K, dev), _dense("dbias", dbias, _f32, N, dev),
+                                _dense("ws", ws, _u8, wsb, dev), wsb, _stream(stream)))
+    return dw
+
+
+def bqm_act_grad(dy, z, act, dz, stream=None):
+    """dz = dy act'(z), element by element."""
+    lib, dev = _begin()
+    n = dy.numel()
+    _check(lib.bqm_act_grad(_dense("dy", dy, _bf16, n, dev), _dense("z", z, _bf16, n, dev), act, n,
+                            _dense("dz", dz, _bf16, n, dev), _stream(stream)))
+    return dz

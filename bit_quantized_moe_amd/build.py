@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libbqm.so")
 
-SOURCES = ["api.hip", "quant.hip", "route.hip", "moe.hip", "mx.hip", "ckpt.hip", "router.hip", "rows.hip"]
+SOURCES = ["api.hip", "quant.hip", "route.hip", "moe.hip", "mx.hip", "ckpt.hip", "router.hip", "rows.hip", "linear.hip"]
 # Bit-exact number-format code: no contraction of a*b+c into fma.
 NO_CONTRACT = {"quant.hip", "route.hip", "api.hip"}
 

@@ -327,6 +327,47 @@ bqm_status bqm_combine_grad(const uint16_t *dout, const uint16_t *y, const int32
                             int64_t H, int32_t k, const int32_t *n_rows, uint16_t *dy, float *dtopk_w, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * The dense product that stands beside the routed experts (a shared expert, a dense layer):
+ * bf16 weights w [N, K], M rows.  M >= 0; N and K multiples of 8 in [8, 2^22); M < 2^31.
+ * Products are exact in FP32, sums FP32; each output is rounded once.
+ *
+ * act: with s(v) = 1 / (1 + e^-v),
+ *   BQM_ACT_SILU       v s(v)
+ *   BQM_ACT_GELU_TANH  v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2
+ *   BQM_ACT_RELU       max(v, 0), whose derivative at 0 is taken as 0
+ *
+ * ws: bqm_linear_workspace_size() bytes of device scratch, for partial sums where the
+ * contraction is split over workgroups (0 bytes, and NULL, where no direction needs any); the
+ * size covers all three directions.  Calls that share one ws must not overlap.  Results are
+ * the same bits in every call with the same sizes. */
+typedef enum { BQM_ACT_NONE = 0, BQM_ACT_RELU = 1, BQM_ACT_SILU = 2, BQM_ACT_GELU_TANH = 3 } bqm_act;
+
+size_t bqm_linear_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/* z = x w^T + bias, y = act(z) + residual.  x bf16 [M, K]; bias bf16 [N] or NULL; residual
+ * bf16 [M, N] or NULL, may be y; y bf16 [M, N]; z bf16 [M, N] or NULL: the pre-activation, for
+ * the backward (y is computed from the FP32 z). */
+bqm_status bqm_linear_fwd(const uint16_t *x, const uint16_t *w, const uint16_t *bias, int32_t act,
+                          const uint16_t *residual, int64_t M, int64_t N, int64_t K, uint16_t *y, uint16_t *z, void *ws,
+                          size_t ws_bytes, void *stream);
+
+/* Gradient of the input: dx = (dz w) act'(zx) + add.  dz bf16 [M, N] is the gradient of z; zx
+ * bf16 [M, K] the pre-activation whose act made x (NULL with BQM_ACT_NONE), so that dx is the
+ * dz of the layer before; add bf16 [M, K] or NULL (the gradient that reaches x by another
+ * way), may be dx; dx bf16 [M, K]. */
+bqm_status bqm_linear_dgrad(const uint16_t *dz, const uint16_t *w, const uint16_t *zx, int32_t act, const uint16_t *add,
+                            int64_t M, int64_t N, int64_t K, uint16_t *dx, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradients of weight and bias: dw f32 [N, K] = dz^T x, dbias f32 [N] (or NULL) = sum over
+ * rows of dz; with accumulate != 0 they are added to what dw and dbias hold. */
+bqm_status bqm_linear_wgrad(const uint16_t *dz, const uint16_t *x, int32_t accumulate, int64_t M, int64_t N, int64_t K,
+                            float *dw, float *dbias, void *ws, size_t ws_bytes, void *stream);
+
+/* dz = dy act'(z) over n elements (bf16), where the activation is a layer's last step; dz may
+ * be dy or z. */
+bqm_status bqm_act_grad(const uint16_t *dy, const uint16_t *z, int32_t act, int64_t n, uint16_t *dz, void *stream);
+
+/* ---------------------------------------------------------------------------
  * The MoE layer.  Expert weights are stacks w_gu [E, 2I, H] (gate rows 0..I-1,
  * up rows I..2I-1, the chunk(2, -1) split of the nf4moe module) and w_dn
  * [E, H, I], both rowwise quantized (NVFP4 per-tensor, or NF4).  LoRA per
