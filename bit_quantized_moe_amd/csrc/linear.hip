@@ -5,7 +5,7 @@
 //   dw = dz^T x, db = sum_m dz                                       (bqm_linear_wgrad)
 //   dz = dy act'(z)                                                  (bqm_act_grad)
 //
-// All three products are C[i, j] = sum_c A(i, c) B(j, c) of bf16 operands on the 32x32x16
+// All three products are C[i, j] = sum_c A(i, c) B(j, c) of bf16 operands on the 16x16x32
 // MFMA with FP32 accumulators.  They differ in how an operand lies in memory: with its
 // contraction contiguous (x and w in the forward, dz in the input gradient) or as rows of the
 // contraction (w in the input gradient, dz and x in the weight gradient); the latter is read
@@ -18,7 +18,6 @@ namespace bqm {
 namespace {
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
-typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(4))) int i32x4;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
@@ -26,10 +25,11 @@ typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(8))) short s16x8;
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
 
 constexpr int NTHR = 256;  // four waves, one per SIMD
-constexpr int KS = 64;     // contraction per step: 128 bytes of a row
 constexpr int kCUs = 256;
+constexpr int KS = 64;  // contraction per step: 128 bytes of a row
 
 enum Mode { FWD, DGRAD, WGRAD };
 
@@ -137,11 +137,13 @@ __device__ __forceinline__ const uint8_t *uniform(const void *q) {
 __device__ __forceinline__ void dma_b128(const void *g, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(g), "s"(lds) : "memory", "m0");
 }
+// The same with a scalar base and a lane's byte offset; lane i's 16 bytes land at lds + AT + 16 i.
+template <int AT>
 __device__ __forceinline__ void dma_b128(const void *base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+  asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :
-               : "v"(off), "s"(uniform(base)), "s"(lds)
-               : "memory", "m0");
+               : "v"(off), "s"(uniform(base)), "s"(__builtin_amdgcn_readfirstlane(lds)), "n"(AT)
+               : "memory", "m0", "scc");
 }
 __device__ __forceinline__ void barrier_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 template <int N>
@@ -159,77 +161,126 @@ __device__ __align__(16) const uint32_t c_zeros[4] = {0u, 0u, 0u, 0u};
 // one operand of a tile
 // ---------------------------------------------------------------------------
 // R result rows (or columns) of it by KS of the contraction per stage.
-// T = false: [row][128 bytes], the 16-byte chunk c of a row at c ^ ((row >> 1) & 7), so that a
-// fragment read (one chunk of 32 rows) falls on different banks.
-// T = true: for each 64 result columns [contraction row][128 bytes], chunk c at c ^ 2 (row & 3):
-// a transposing read takes 32 bytes of 4 rows per 16 lanes.
-// Stages are filled by direct copies of 1 KB (8 of those 128-byte rows) per wave.
+// T = false: [row][KS], the 16-byte chunk c of a row at c ^ ((row >> 1) & (chunks - 1)), so that
+// a fragment read (one chunk of 16 rows) falls on different banks.
+// T = true: for each 64 result columns [contraction row][128 bytes], chunk c of row r at
+// c ^ 2 ((r & 3) ^ (r / 8 & 1)): a transposing read takes 32 bytes of rows 0..3 and 8..11 per
+// 32 lanes.
+// Stages are filled by direct copies of 1 KB per wave: 512 / KS rows, or 8 of the 128-byte rows.
 template <int R, bool T, bool FAST>
 struct Operand {
-  static constexpr int kCopies = R / 32;  // per wave and step
+  static constexpr int kCopies = R * KS / 2048;  // per wave and step
+  static constexpr int CPR = KS / 8;             // chunks per row
   const uint8_t *base;
   int64_t ld;
   uint32_t off[kCopies];
   int C;
   int lane, w;
 
+  // row (of the result, or with T of the contraction) and result column of copy j of this lane
+  __device__ __forceinline__ int row(int j) const {
+    const int n = kCopies * w + j;
+    return T ? 8 * (n % CPR) + (lane >> 3) : 512 / KS * n + lane / CPR;
+  }
+  __device__ __forceinline__ int chunk(int j) const {
+    const int r = row(j);
+    return T ? (lane & 7) ^ turn(r) : (lane & (CPR - 1)) ^ ((r >> 1) & (CPR - 1));
+  }
+
+  // T: what a row's chunks are XORed with
+  __device__ __forceinline__ static int turn(int r) { return 2 * ((r & 3) ^ ((r >> 3) & 1)); }
+
   // rows: of the whole operand; r0: the tile's first
   __device__ __forceinline__ void setup(const uint8_t *q, int64_t ld_, int C_, int64_t rows, int64_t r0, int lane_, int w_) {
     ld = ld_, C = C_, lane = lane_, w = w_;
     base = uniform(T ? q + 2 * r0 : q + r0 * ld);
+    const int most = (int)min(rows - r0, (int64_t)R);
 #pragma unroll
     for (int j = 0; j < kCopies; ++j) {
-      const int n = kCopies * w + j;
+      if constexpr (T)  // columns past the last are the last 8 again (their results are dropped)
+        off[j] = (uint32_t)row(j) * (uint32_t)ld + 2 * min(64 * ((kCopies * w + j) / CPR) + 8 * chunk(j), most - 8);
+      else
+        off[j] = (uint32_t)min(row(j), most - 1) * (uint32_t)ld + 16 * chunk(j);
+    }
+  }
+
+  // copy J of step ks.  FAST: a contraction of at least one whole step; the last step, where
+  // it is not whole, takes the last KS of the contraction (and zeroes in registers what the
+  // step before had).  Otherwise the one step there is takes zeros past the end.
+  template <int J>
+  __device__ __forceinline__ void copy(int ks, uint8_t *stage) const {
+    const uint32_t to = lds_addr(stage) + 1024 * kCopies * w;
+    if constexpr (FAST) {
+      const int at = min(KS * ks, C - KS);
+      dma_b128<1024 * J>(base + (T ? at * ld : (int64_t)(2 * at)), off[J], to);
+    } else {
+      const bool in = T ? row(J) < C : 8 * chunk(J) < C;
+      dma_b128(in ? base + off[J] : reinterpret_cast<const uint8_t *>(c_zeros), to + 1024 * J);
+    }
+  }
+
+  // Fragment of 16 rows from row c0 + c on (c0: the wave's), slice kk: lane l holds row l % 16,
+  // contraction 32 kk + 8 (l / 16) + 0..7.  Its address is one of a few that depend on the
+  // lane (kept in registers, one addition per stage), and a constant.
+  static constexpr int kVariants = T ? 4 : 2;  // by c / 16 % 4, by kk
+  uint32_t lane_at[kVariants];
+  __device__ __forceinline__ void setup_fragments(int c0) {
+#pragma unroll
+    for (int v = 0; v < kVariants; ++v) {
       if constexpr (T) {
-        const int r = 8 * (n & 7) + (lane >> 3), c = 64 * (n >> 3) + 8 * ((lane & 7) ^ (2 * (r & 3)));
-        // columns past the last are the last 8 again (their results are dropped)
-        const int most = (int)min(rows - r0, (int64_t)R) - 8;
-        off[j] = (uint32_t)r * (uint32_t)ld + 2 * min(c, most);
+        const int g = lane >> 4, s = lane & 15, c = c0 + 16 * v;
+        lane_at[v] = (c >> 6) * (KS * 128) + (8 * g + (s >> 2)) * 128 +
+                     16 * (((c & 63) / 8 + ((s & 3) >> 1)) ^ turn(8 * g + (s >> 2))) + 8 * (s & 1);
       } else {
-        const int r = 8 * n + (lane >> 3), most = (int)min(rows - r0, (int64_t)R) - 1;
-        off[j] = (uint32_t)min(r, most) * (uint32_t)ld + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+        const int r = c0 + (lane & 15);
+        lane_at[v] = r * (2 * KS) + 16 * ((4 * v + (lane >> 4)) ^ ((r >> 1) & (CPR - 1)));
       }
     }
   }
-
-  // copy j of step ks.  FAST: a contraction of at least one whole step; the last step, where
-  // it is not whole, takes the last KS of the contraction (and zeroes in registers what the
-  // step before had).  Otherwise the one step there is takes zeros past the end.
-  __device__ __forceinline__ void copy(int j, int ks, uint8_t *stage) const {
-    const uint32_t to = lds_addr(stage) + 1024 * (kCopies * w + j);
-    if constexpr (FAST) {
-      const int at = min(KS * ks, C - KS);
-      dma_b128(base + (T ? at * ld : (int64_t)(2 * at)), off[j], to);
-    } else {
-      const int n = kCopies * w + j, r = 8 * n + (lane >> 3);
-      const bool in = T ? (r & 63) < C : 8 * ((lane & 7) ^ ((r >> 1) & 7)) < C;
-      dma_b128(in ? base + off[j] : reinterpret_cast<const uint8_t *>(c_zeros), to);
+  // the fragments' addresses in a stage; opaque, or the compiler adds the constants to the
+  // stage first, and then the lane's part to each of the sums
+  uint32_t at[kVariants];
+  __device__ __forceinline__ void enter(uint32_t stage) {
+#pragma unroll
+    for (int v = 0; v < kVariants; ++v) {
+      at[v] = stage + lane_at[v];
+      asm("" : "+v"(at[v]));
     }
   }
-
-  // fragment of 32 rows from row c on, slice kk: lane l holds row l % 32, contraction
-  // 16 kk + 8 (l / 32) + 0..7
-  __device__ __forceinline__ i32x4 fragment(const uint8_t *stage, int c, int kk) const {
+  // c: a multiple of 16, known when compiled
+  __device__ __forceinline__ i32x4 fragment(int c, int kk) const {
     if constexpr (T) {
-      const int g = lane >> 4, s = lane & 15;
-      const uint8_t *q = stage + (c >> 6) * (KS * 128) + (16 * kk + 8 * (g >> 1) + (s >> 2)) * 128 +
-                         16 * (((c & 63) / 8 + 2 * (g & 1) + ((s & 3) >> 1)) ^ (2 * (s >> 2))) + 8 * (s & 1);
-      const s16x4 h0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(q));
-      const s16x4 h1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(q + 4 * 128));
+      const uint32_t q = at[c / 16 % 4] + (c >> 6) * (KS * 128) + kk * (32 * 128);
+      const s16x4 h0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(q));
+      const s16x4 h1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(q + 4 * 128));
       const s16x8 v = {h0[0], h0[1], h0[2], h0[3], h1[0], h1[1], h1[2], h1[3]};
       return __builtin_bit_cast(i32x4, v);
     } else {
-      const int r = c + (lane & 31);
-      return *reinterpret_cast<const i32x4 *>(stage + r * 128 + 16 * ((2 * kk + (lane >> 5)) ^ ((r >> 1) & 7)));
+      return *(const lds_i32x4 *)(uintptr_t)(at[kk] + c * (2 * KS));
     }
   }
 };
 
-template <int BM, int BN, int NS>
+// OUT: bytes of the epilogue for each wave; 0: it takes the stages
+template <int BM, int BN, int NSA, int NSB, int OUT>
 struct Smem {
-  uint8_t a[NS][BM * 128];
-  uint8_t b[NS][BN * 128];
+  uint8_t a[NSA][BM * 2 * KS];
+  uint8_t b[NSB][BN * 2 * KS];
+  uint8_t out[4][OUT];
 };
+template <int BM, int BN, int NSA, int NSB>
+struct Smem<BM, BN, NSA, NSB, 0> {
+  uint8_t a[NSA][BM * 2 * KS];
+  uint8_t b[NSB][BN * 2 * KS];
+};
+
+// row and column tile of tile L: groups of about G row tiles, column by column
+template <int G>
+__device__ __forceinline__ int2 tile_at(const LinParams &p, int L) {
+  const int n_g = max((p.NI + G / 2) / G, 1), g = (p.NI + n_g - 1) / n_g;
+  const int m_first = L / (g * p.NJ) * g, gm = min(g, p.NI - m_first), in_g = L - m_first * p.NJ;
+  return make_int2(m_first + in_g % gm, in_g / gm);
+}
 
 // ---------------------------------------------------------------------------
 // a tile
@@ -237,243 +288,510 @@ struct Smem {
 // A workgroup of four waves (WM x WN) computes BM = 32 WM TM rows by BN = 32 WN TN columns;
 // wave (wm, wn) owns the 32-row tiles WM tm + wm (interleaved, so that a partly filled tile
 // leaves all rows of waves the same work) of 32 TN columns.  The contraction goes in steps of
-// KS through NS LDS stages; a step is four slices of VT x TN MFMAs.  One wave per SIMD (the
+// KS through NS LDS stages; a step is KS / 32 slices of 2 VT x 2 TN MFMAs.  One wave per SIMD (the
 // accumulators of the largest tile take half the register file) has no other wave to hide its
 // waits behind, so a step is written out in issue order: each MFMA is followed by its share of
 // the fragment reads of the next slice and of the copies of a later step, held there by
-// scheduling barriers.  The step's one barrier sits inside slice 3, whose fragments are in
-// registers by then; the copies of step ks + NS start behind it, into the stage just read.
+// scheduling barriers.  The step's one barrier sits inside its last slice, whose fragments are
+// in registers by then; the copies of step ks + NS start behind it, into the stage just read.
 //
-// Accumulators hold the product transposed (B x A): register v of lane L of tile (tm, tn) is
-// row L % 32 and column 8 (v / 4) + 4 (L / 32) + v % 4.
-template <int WM, int TM, int TN, bool AT, bool BT, bool FAST, int NS>
+// Accumulators hold the product transposed (B x A): register v of lane L of a 16 x 16 block is
+// row L % 16 and column 4 (L / 16) + v.
+template <int WM, int TM, int TN, bool AT, bool BT, bool FAST, int NSA, int NSB>
 struct Tile {
   static constexpr int WN = 4 / WM, BM = 32 * WM * TM, BN = 32 * WN * TN;
-  static constexpr int CA = BM / 32, CB = BN / 32, kCopies = CA + CB, kFirst = kCopies / 2;
+  using OpA = Operand<BM, AT, FAST>;
+  using OpB = Operand<BN, BT, FAST>;
+  static constexpr int CA = OpA::kCopies, CB = OpB::kCopies, kCopies = CA + CB;
+  static constexpr int NSL = KS / 32;  // slices per step
+  static constexpr bool WHOLE = TM * TN == 1;  // fragments of a whole step in registers, twice
+  static constexpr int RM = 2 * TM, RN = 2 * TN;    // fragments of 16 rows, of 16 columns
+  // sets of fragments; WHOLE: set NSL q + kk for slice kk of a step of parity q
+  static constexpr int SETS_A = WHOLE ? 2 * NSL : 1, SETS_B = WHOLE ? 2 * NSL : 2;
+  static_assert(WHOLE ? NSA == NSB : NSL == 2 && (NSA == NSB || NSA == NSB + 1), "stages");
+  static constexpr int UN = TN < 2 ? 1 : 2;  // column tiles of a unit of the epilogue
+  static constexpr int CH = 8 * UN, LPR = 4 * UN, RP = 64 / LPR, NP = 32 / RP;
+  using Mem = Smem<BM, BN, NSA, NSB, WHOLE ? 32 * CH * 16 : 0>;
+  static constexpr int NS = NSB;  // WHOLE: of both
   const LinParams &p;
-  Smem<BM, BN, NS> &sm;
+  Mem &sm;
   int lane, w, wm, wn;
-  Operand<BM, AT, FAST> a;
-  Operand<BN, BT, FAST> b;
+  OpA a;
+  OpB b;
   int over;  // of the last step, the leading part that the step before had
-  i32x4 af[2][TM], bf[2][TN];
-  f32x16 acc[TM][TN];
+  i32x4 af[SETS_A][RM], bf[SETS_B][RN];
+  f32x4 acc[RM][RN];
+  // where a lane's share of the result goes
+  struct Out {
+    int64_t first;      // element offset of the wave's first row and column in the result
+    uint32_t off;       // of this lane's from there
+    int rows, cols;     // of the result from this lane's first on
+    bool whole;         // all of the tile exists
+    float *part;
+    const uint16_t *bias;
+  };
 
-  __device__ __forceinline__ Tile(const LinParams &p_, Smem<BM, BN, NS> &sm_) : p(p_), sm(sm_) {
+  __device__ __forceinline__ Tile(const LinParams &p_, Mem &sm_) : p(p_), sm(sm_) {
     lane = threadIdx.x & 63;
     w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     wm = WM == 2 ? w >> 1 : 0;
     wn = WM == 2 ? w & 1 : w;
   }
 
-  __device__ __forceinline__ void copy(int j, int ks) {
-    if (j < CA)
-      a.copy(j, ks, sm.a[ks & (NS - 1)]);
+  __device__ __forceinline__ static int stage_a(int ks) { return (int)((unsigned)ks % NSA); }
+  __device__ __forceinline__ static int stage_b(int ks) { return (int)((unsigned)ks % NSB); }
+  template <int J>
+  __device__ __forceinline__ void copy_a(int ks) {
+    a.template copy<J>(ks, sm.a[stage_a(ks)]);
+  }
+  template <int J>
+  __device__ __forceinline__ void copy_b(int ks) {
+    b.template copy<J>(ks, sm.b[stage_b(ks)]);
+  }
+  template <int J = 0>
+  __device__ __forceinline__ void copy_step(int ks) {  // B, then A
+    if constexpr (J < CB)
+      copy_b<J>(ks);
     else
-      b.copy(j - CA, ks, sm.b[ks & (NS - 1)]);
+      copy_a<J - CB>(ks);
+    if constexpr (J + 1 < kCopies) copy_step<J + 1>(ks);
   }
-  // the i-th of a slice's reads, in the order its MFMAs ask for them
-  __device__ __forceinline__ void read(int k, int i, int kk, int st) {
-    if (i == 0 || i > TN) {
-      const int tm = i == 0 ? 0 : i - TN;
-      af[k][tm] = a.fragment(sm.a[st], 32 * (WM * tm + wm), kk);
-    } else {
-      bf[k][i - 1] = b.fragment(sm.b[st], 32 * (wn * TN + i - 1), kk);
-    }
+  // fragments are read from the stages of step ks from here on
+  __device__ __forceinline__ void enter(int ks) {
+    a.enter(lds_addr(sm.a[0]) + stage_a(ks) * (uint32_t)sizeof(sm.a[0]));
+    b.enter(lds_addr(sm.b[0]) + stage_b(ks) * (uint32_t)sizeof(sm.b[0]));
   }
-  __device__ __forceinline__ void mfma(int k, int tm, int tn) {
-    acc[tm][tn] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, bf[k][tn]),
-                                                          __builtin_bit_cast(bf16x8, af[k][tm]), acc[tm][tn], 0, 0, 0);
+  // a wave's 32-row tiles are 32 WM rows apart
+  __device__ __forceinline__ void read_a(int k, int m, int kk) { af[k][m] = a.fragment(32 * WM * (m / 2) + 16 * (m % 2), kk); }
+  __device__ __forceinline__ void read_b(int k, int n, int kk) { bf[k][n] = b.fragment(16 * n, kk); }
+  // the q-th of a slice's MFMAs
+  __device__ __forceinline__ void mfma(int ka, int kb, int q) {
+    const int m = q / RN, n = q % RN;
+    acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bf[kb][n]),
+                                                        __builtin_bit_cast(bf16x8, af[ka][m]), acc[m][n], 0, 0, 0);
   }
 
   // zeros in place of what the step before the last had, in both operands (0 times an
   // infinity would be NaN)
   template <int VT>
-  __device__ __forceinline__ void drop_overlap(int kk) {
-    if (over <= 16 * kk) return;
+  __device__ __forceinline__ void drop_overlap(int ka, int kb, int kk) {
+    if (over <= 32 * kk) return;
     int mask[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int d = over - (16 * kk + 8 * (lane >> 5) + 2 * i);
+      const int d = over - (32 * kk + 8 * (lane >> 4) + 2 * i);
       mask[i] = d <= 0 ? -1 : d == 1 ? (int)0xFFFF0000 : 0;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int tm = 0; tm < VT; ++tm) af[kk & 1][tm][i] &= mask[i];
+      for (int m = 0; m < 2 * VT; ++m) af[ka][m][i] &= mask[i];
 #pragma unroll
-      for (int tn = 0; tn < TN; ++tn) bf[kk & 1][tn][i] &= mask[i];
+      for (int n = 0; n < RN; ++n) bf[kb][n][i] &= mask[i];
     }
   }
 
-  // LEFT: steps that follow, NS for that or more.
-  // slices 0-2: fragment reads of the next slice; in slice 0 first the copies that slice 3 of
-  // the step before has not begun
-  template <int VT, int KK, int LEFT>
+  // Large tiles: a slice is 2 VT x RN MFMAs, row of fragments by row.  Beside them go, evenly
+  // spread, the fragment reads of the next slice.  A row's fragment is read into the place of
+  // the one just used, the last one at the start of its slice; B has two sets (two sets of both
+  // leave too few registers).  Slice 1 has the step's barrier behind its first row, from where
+  // on this step's stages are filled anew: with B for step ks + NSB, then A for ks + NSA, which
+  // goes on in slice 0 of the next step.  The copies are kGap MFMAs apart: the four waves' take
+  // 64 cycles on their way, and closer ones hold up the MFMAs; B, with fewer stages, comes first
+  // as it has the least time.
+  static constexpr int kGap = 5;
+  // MFMAs between the barrier and copy j of a step
+  template <int VT>
+  __device__ __forceinline__ static constexpr int copy_at(int j) {
+    constexpr int all = 3 * VT * RN + (VT - 1) * RN, gap = kGap * kCopies < all ? kGap : 0;
+    if (!gap) return j * all / kCopies;
+    return j < CB ? gap * j : gap * CB + (j - CB) * (all - gap * CB) / CA;
+  }
+  template <int VT, int J>
+  __device__ __forceinline__ void copies_at(int at, int s) {
+    if (copy_at<VT>(J) == at) {
+      if constexpr (J < CB)
+        copy_b<J>(s + NSB);
+      else
+        copy_a<J - CB>(s + NSA);
+    }
+    if constexpr (J + 1 < kCopies) copies_at<VT, J + 1>(at, s);
+  }
+  // of A's copies of a step, those from J on that come before the next step's slice 0
+  template <int VT, int J = 0>
+  __device__ __forceinline__ void first_copies_a(int ks) {
+    if constexpr (J < CA) {
+      if constexpr (copy_at<VT>(CB + J) < (2 * VT - 1) * RN) copy_a<J>(ks);
+      first_copies_a<VT, J + 1>(ks);
+    }
+  }
+  template <int VT>
+  static constexpr int count_first() {
+    int n = 0;
+    for (int j = 0; j < CA; ++j) n += copy_at<VT>(CB + j) < (2 * VT - 1) * RN;
+    return n;
+  }
+  template <int J = 0>
+  __device__ __forceinline__ void copies_b(int ks) {
+    copy_b<J>(ks);
+    if constexpr (J + 1 < CB) copies_b<J + 1>(ks);
+  }
+  template <int VT, int KK, bool LAST>
   __device__ __forceinline__ void slice(int ks) {
-    if constexpr (FAST && LEFT == 0) drop_overlap<VT>(KK);
-    constexpr int NP = VT * TN, NC = KK == 0 && LEFT >= NS - 1 ? kCopies - kFirst : 0, NI = NC + TN + VT;
+    constexpr int R = 2 * VT, NP = R * RN, QB = RN, NR = LAST && KK == 1 ? 0 : RN + R - 1, Q0 = KK == 1 ? QB : 0;
+    read_a(0, R - 1, KK);
+    if constexpr (FAST && LAST) drop_overlap<VT>(0, KK, KK);
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
-      mfma(KK & 1, q / TN, q % TN);
-#pragma unroll
-      for (int i = q * NI / NP; i < (q + 1) * NI / NP; ++i) {
-        if (i < NC)
-          copy(kFirst + i, ks - 1 + NS);
-        else
-          read((KK + 1) & 1, i - NC, KK + 1, ks & (NS - 1));
-      }
-      LIN_PIN();
-    }
-  }
-  template <int VT, int LEFT>
-  __device__ __forceinline__ void slice3(int ks) {
-    if constexpr (FAST && LEFT == 0) drop_overlap<VT>(3);
-    constexpr int NP = VT * TN, NR = TN + VT, NC = LEFT >= NS ? kFirst : 0, NI = NR + NC;
-    constexpr int both = NC < NR ? NC : NR;
-#pragma unroll
-    for (int q = 0; q < NP; ++q) {
-      mfma(1, q / TN, q % TN);
-      if constexpr (LEFT > 0) {
-        if (q == 0) {
-          // every wave is done reading this stage, and the next is whole
+      mfma(0, KK, q);
+      if constexpr (KK == 1 && !LAST) {
+        if (q == QB - 1) {
+          // every wave is done reading this step's stages, and the next are whole
           LIN_PIN();
-          wait_vm<(LEFT - 1 < NS - 2 ? LEFT - 1 : NS - 2) * kCopies>();
+          wait_vm<(NSB - 2) * kCopies + (NSA > NSB ? CA : 0)>();
           barrier_lds();
+          enter(ks + 1);
           LIN_PIN();
         }
+      }
+      if (q >= QB) {  // a row's fragment has been used
 #pragma unroll
-        for (int i = q * NI / NP; i < (q + 1) * NI / NP; ++i) {
-          // in turn a copy and a read, as long as there are both
-          const bool isc = i < 2 * both ? !(i & 1) : NC > both;
-          const int j = i < 2 * both ? i >> 1 : i - both;
-          if (isc)
-            copy(j, ks + NS);
+        for (int i = (q - QB) * NR / (NP - QB); i < (q - QB + 1) * NR / (NP - QB); ++i) {
+          if (i < RN)
+            read_b(KK ^ 1, i, KK ^ 1);
           else
-            read(0, j, 0, (ks + 1) & (NS - 1));
+            read_a(0, i - RN, KK ^ 1);
         }
       }
+      if (!LAST && q >= Q0) copies_at<VT, 0>(KK == 1 ? q - QB : NP - QB + q, KK == 1 ? ks : ks - 1);
       LIN_PIN();
     }
-  }
-  template <int VT, int LEFT>
-  __device__ __forceinline__ void step(int ks) {
-    slice<VT, 0, LEFT>(ks);
-    slice<VT, 1, LEFT>(ks);
-    slice<VT, 2, LEFT>(ks);
-    slice3<VT, LEFT>(ks);
-  }
-  template <int VT, int LEFT>
-  __device__ __forceinline__ void tail(int &ks, int last) {
-    if (last - ks == LEFT) step<VT, LEFT>(ks++);
-    if constexpr (LEFT > 0) tail<VT, LEFT - 1>(ks, last);
   }
 
-  // steps [k0, k1) of the tile at (i0, j0), of which VT row tiles per wave hold rows
+  // zeros as products of zeros: short code
+  template <int VT>
+  __device__ __forceinline__ void clear() {
+    bf16x8 z = {};
+    asm volatile("" : "+v"(z));
+#pragma unroll
+    for (int m = 0; m < 2 * VT; ++m)
+#pragma unroll
+      for (int n = 0; n < RN; ++n) acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z, z, f32x4{}, 0, 0, 0);
+  }
+
+  // Small tiles: a slice's few MFMAs are shorter than a fragment read takes, so all of the next
+  // step's fragments are read while this step's are multiplied.
+  template <int VT>
+  __device__ __forceinline__ void read_step(int ks, int par) {
+    enter(ks);
+#pragma unroll
+    for (int kk = 0; kk < NSL; ++kk) {
+#pragma unroll
+      for (int i = 0; i < RN; ++i) read_b(NSL * par + kk, i, kk);
+#pragma unroll
+      for (int i = 0; i < 2 * VT; ++i) read_a(NSL * par + kk, i, kk);
+    }
+  }
+  template <int VT>
+  __device__ __forceinline__ void mfma_step(int par) {
+#pragma unroll
+    for (int kk = 0; kk < NSL; ++kk)
+#pragma unroll
+      for (int q = 0; q < 2 * VT * RN; ++q) mfma(NSL * par + kk, NSL * par + kk, q);
+  }
+  // waits until at most min(n, N) steps' copies are in flight
+  template <int N>
+  __device__ __forceinline__ static void wait_steps(int n) {
+    if (N == 0 || n >= N)
+      wait_vm<N * kCopies>();
+    else if constexpr (N > 0)
+      wait_steps<N - 1>(n);
+  }
+  // MORE: at least NS steps follow
+  template <int VT, int PAR, bool MORE>
+  __device__ __forceinline__ void whole_step(int ks, int last) {
+    wait_steps<NS - 2>(MORE ? NS : last - ks - 1);
+    barrier_lds();  // the next step's stage is whole, and every wave has this step's fragments
+    read_step<VT>(ks + 1, PAR ^ 1);
+    if (MORE || ks + NS <= last) copy_step(ks + NS);
+    mfma_step<VT>(PAR);
+  }
+  template <int VT, int PAR>
+  __device__ __forceinline__ void last_step() {
+    if constexpr (FAST) {
+#pragma unroll
+      for (int kk = 0; kk < NSL; ++kk) drop_overlap<VT>(NSL * PAR + kk, NSL * PAR + kk, kk);
+    }
+    mfma_step<VT>(PAR);
+  }
+  template <int VT>
+  __device__ __forceinline__ void run_whole(int k0, int last) {
+#pragma unroll
+    for (int q = 0; q < NS; ++q)
+      if (k0 + q <= last) copy_step(k0 + q);
+    clear<VT>();
+    wait_steps<NS - 1>(last - k0);
+    barrier_lds();
+    read_step<VT>(k0, 0);
+    int ks = k0;
+    for (; ks + NS + 1 <= last; ks += 2) {
+      whole_step<VT, 0, true>(ks, last);
+      whole_step<VT, 1, true>(ks + 1, last);
+    }
+    for (; ks + 2 <= last; ks += 2) {
+      whole_step<VT, 0, false>(ks, last);
+      whole_step<VT, 1, false>(ks + 1, last);
+    }
+    if (ks < last) {
+      whole_step<VT, 0, false>(ks, last);
+      last_step<VT, 1>();
+    } else {
+      last_step<VT, 0>();
+    }
+  }
+
+  // steps [k0, k1) of the tile, of which VT row tiles per wave hold rows
   template <int VT>
   __device__ __forceinline__ void run(int k0, int k1) {
-#pragma unroll
-    for (int tm = 0; tm < VT; ++tm)
-#pragma unroll
-      for (int tn = 0; tn < TN; ++tn)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) acc[tm][tn][v] = 0.0f;
     over = FAST && k1 == p.nk ? KS * p.nk - p.C : 0;
-    const int last = k1 - 1;
-#pragma unroll
-    for (int q = 0; q < NS - 1; ++q)
-      if (k0 + q <= last) {
-#pragma unroll
-        for (int j = 0; j < kCopies; ++j) copy(j, k0 + q);
-      }
-    if (NS == 2 || last - k0 < NS - 2)
-      wait_vm<0>();
+    if constexpr (WHOLE)
+      run_whole<VT>(k0, k1 - 1);
     else
-      wait_vm<(NS - 2) * kCopies>();
-    barrier_lds();
+      run_sliced<VT>(k0, k1 - 1);
+  }
+
+  // The copies run up to NSA steps past the last (where FAST has them end within the operand)
+  // and are not used: one loop body for all steps but the last keeps the code that a workgroup
+  // executes short, and its first pass over it is bound by the instruction fetch.
+  template <int VT>
+  __device__ __forceinline__ void run_sliced(int k0, int last) {
+    // in the order of the loop; its first slice 0 has the rest
 #pragma unroll
-    for (int i = 0; i < TN + VT; ++i) read(0, i, 0, k0 & (NS - 1));
-    if (k0 + NS - 1 <= last) {
-#pragma unroll
-      for (int j = 0; j < kFirst; ++j) copy(j, k0 + NS - 1);
+    for (int q = 0; q < NSB; ++q) {
+      if (q < NSA - 1) {
+        copy_step(k0 + q);
+      } else {
+        copies_b(k0 + q);
+        first_copies_a<VT>(k0 + q);
+      }
     }
-    int ks = k0;
-    for (; ks + NS <= last; ++ks) step<VT, NS>(ks);
-    tail<VT, NS - 1>(ks, last);
+    if constexpr (NSA > NSB) first_copies_a<VT>(k0 + NSB);
+    constexpr int rest = NSA > NSB ? NSB : NSA - 1;  // whole steps of A, of which one is needed
+    clear<VT>();
+    wait_vm<(NSB - 1) * CB + (rest - 1) * CA + count_first<VT>()>();
+    barrier_lds();
+    enter(k0);
+#pragma unroll
+    for (int i = 0; i < RN; ++i) read_b(0, i, 0);
+#pragma unroll
+    for (int i = 0; i < 2 * VT - 1; ++i) read_a(0, i, 0);
+    for (int ks = k0; ks < last; ++ks) {
+      slice<VT, 0, false>(ks);
+      slice<VT, 1, false>(ks);
+    }
+    slice<VT, 0, true>(last);
+    slice<VT, 1, true>(last);
+    // the epilogue takes the stages: no copy lands there, no wave reads them any more
+    wait_vm<0>();
+    barrier_lds();
   }
 
-  // 32 rows of the wave to its part t of LDS
-  template <int TMX>
+  // The accumulators hold 4 columns of 16 rows a lane quarter.  They pass through LDS in FP32 in
+  // units of 32 rows by UN column tiles of a wave, so that a lane finishes 8 consecutive columns
+  // of NP rows and reads and writes 16 bytes at a time (chunk c of row r at c ^ (r & (CH - 1))).
+  // One wave per SIMD means that every instruction here counts: addresses are a scalar base
+  // and a lane offset that stays, choices are made once for all of a lane's values, and what
+  // the epilogue reads (residual, pre-activation) is loaded one unit ahead.
+  static constexpr int MODE = AT ? WGRAD : BT ? DGRAD : FWD;
+  static constexpr int UC = TN / UN;  // units per 32 rows
+
+  template <int TMX, int U>
   __device__ __forceinline__ void put(uint8_t *t) const {
-    constexpr int CH = 8 * TN;
-    const int r = lane & 31;
 #pragma unroll
-    for (int tn = 0; tn < TN; ++tn)
+    for (int m = 0; m < 2; ++m) {
+      const int r = 16 * m + (lane & 15);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<f32x4 *>(t + 16 * (r * CH + ((8 * tn + 2 * q + (lane >> 5)) ^ (r & (CH - 1))))) =
-            f32x4{acc[TMX][tn][4 * q], acc[TMX][tn][4 * q + 1], acc[TMX][tn][4 * q + 2], acc[TMX][tn][4 * q + 3]};
+      for (int n = 0; n < 2 * UN; ++n)
+        *reinterpret_cast<f32x4 *>(t + 16 * (r * CH + ((4 * n + (lane >> 4)) ^ (r & (CH - 1))))) = acc[2 * TMX + m][2 * UN * U + n];
+    }
+    // an end of its own for each: with one end in common the compiler addresses the
+    // accumulators by a variable, and so keeps them in memory
+    asm volatile("; unit %0" ::"n"(TMX * UC + U));
+  }
+  template <int U>
+  __device__ __forceinline__ void put_unit(int tm, uint8_t *t) const {
+    if (TM == 1 || tm == 0)
+      put<0, U>(t);
+    else if (TM == 2 || tm == 1)
+      put<TM < 2 ? 0 : 1, U>(t);
+    else if (tm == 2)
+      put<TM < 4 ? 0 : 2, U>(t);
+    else
+      put<TM < 4 ? 0 : 3, U>(t);
   }
 
-  // The accumulators hold 4 columns of 32 rows a lane quarter.  They pass through LDS in FP32,
-  // 32 rows of a wave at a time, so that a lane finishes 8 consecutive columns of a row and
-  // reads and writes 16 bytes at a time (chunk c of row r at c ^ (r & its number of chunks - 1)).
-  __device__ __forceinline__ void store(int vt, int64_t i0, int64_t j0, float *part) {
-    constexpr int CH = 8 * TN, LPR = 4 * TN, RP = 64 / LPR, NP = 32 / RP, UN = 4;
-    static_assert(sizeof(sm.a) + sizeof(sm.b) >= 4 * 32 * CH * 16, "the waves' parts fit the stages");
-    uint8_t *t = sm.a[0] + w * (32 * CH * 16);
+  __device__ __forceinline__ Out out_of(int64_t i0, int64_t j0, float *part) const {
+    Out o;
     const int lr = lane / LPR, c = lane % LPR;
-    const int col = 32 * TN * wn + 8 * c;
-    const bool cin = j0 + col < p.J;
-    u32x4 bias = {};
-    if (!part && p.mode == FWD && p.bias && cin) bias = load8(p.bias + j0 + col);
-    barrier_lds();  // every wave is done with the stages
-#pragma unroll 1
-    for (int tm = 0; tm < vt; ++tm) {
-      const int r0 = 32 * (WM * tm + wm);
-      if (TM == 1 || tm == 0)
-        put<0>(t);
-      else if (TM == 2 || tm == 1)
-        put<TM < 2 ? 0 : 1>(t);
-      else if (tm == 2)
-        put<TM < 4 ? 0 : 2>(t);
-      else
-        put<TM < 4 ? 0 : 3>(t);
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll 1
-      for (int q0 = 0; q0 < NP; q0 += UN) {
-        Extra x[UN];
-        f32x4 lo[UN], hi[UN];
+    o.first = (i0 + 32 * wm) * p.J + j0 + 32 * TN * wn;
+    o.off = (uint32_t)lr * (uint32_t)p.J + 8 * c;
+    o.rows = (int)min(p.I - i0, (int64_t)BM) - 32 * wm - lr;
+    o.cols = (int)min(p.J - j0, (int64_t)BN) - 32 * TN * wn - 8 * c;
+    o.whole = p.I - i0 >= BM && p.J - j0 >= BN;
+    o.part = part;
+    o.bias = p.bias + j0 + 32 * TN * wn;
+    return o;
+  }
+  // element (32 WM tm, 32 UN u) from the wave's first on
+  __device__ __forceinline__ int64_t unit_at(int tm, int u) const { return (int64_t)(32 * WM * tm) * p.J + 32 * UN * u; }
+  __device__ __forceinline__ static bool inside(const Out &o, int tm, int u, int q) {
+    return 32 * WM * tm + RP * q < o.rows && 32 * UN * u < o.cols;
+  }
+
+  // what lies outside the result is read from src's first elements instead (and not used)
+  __device__ __forceinline__ void load_rows(const Out &o, const uint16_t *src, int tm, int u, u32x4 *x) const {
+    const uint8_t *base = uniform(src + o.first + unit_at(tm, u));
+    const int64_t pass = (int64_t)RP * p.J * 2;
+    if (o.whole) {
 #pragma unroll
-        for (int q = 0; q < UN; ++q) {
-          const int64_t row = i0 + r0 + (q0 + q) * RP + lr;
-          if (!part && cin && row < p.I) x[q] = load_extra(p, row * p.J + j0 + col);
-        }
+      for (int q = 0; q < NP; ++q) x[q] = *reinterpret_cast<const u32x4 *>(base + q * pass + 2 * o.off);
+    } else {
 #pragma unroll
-        for (int q = 0; q < UN; ++q) {
-          const int rr = (q0 + q) * RP + lr;
-          lo[q] = *reinterpret_cast<const f32x4 *>(t + 16 * (rr * CH + ((2 * c) ^ (rr & (CH - 1)))));
-          hi[q] = *reinterpret_cast<const f32x4 *>(t + 16 * (rr * CH + ((2 * c + 1) ^ (rr & (CH - 1)))));
-        }
+      for (int q = 0; q < NP; ++q)
+        x[q] = load8(inside(o, tm, u, q) ? reinterpret_cast<const uint16_t *>(base + q * pass + 2 * o.off) : src);
+    }
+  }
+  // ADD, ZX: whether there is something to add, and an activation's argument
+  template <bool ADD, bool ZX>
+  struct Extras {
+    u32x4 add[ADD ? NP : 1], zx[ZX ? NP : 1];
+  };
+  template <bool ADD, bool ZX>
+  __device__ __forceinline__ void load_extras(const Out &o, int tm, int u, Extras<ADD, ZX> &x) const {
+    if constexpr (ADD) load_rows(o, p.add, tm, u, x.add);
+    if constexpr (ZX) load_rows(o, p.zx, tm, u, x.zx);
+  }
+  __device__ __forceinline__ void store_rows(const Out &o, uint16_t *dst, int tm, int u, const u32x4 *x) const {
+    uint8_t *base = const_cast<uint8_t *>(uniform(dst + o.first + unit_at(tm, u)));
+    const int64_t pass = (int64_t)RP * p.J * 2;
+    if (o.whole) {
 #pragma unroll
-        for (int q = 0; q < UN; ++q) {
-          const int rr = (q0 + q) * RP + lr;
-          const int64_t row = i0 + r0 + rr;
-          if (cin && row < p.I) {
-            if (part) {
-              f32x4 *o = reinterpret_cast<f32x4 *>(part + (r0 + rr) * BN + col);
-              o[0] = lo[q];
-              o[1] = hi[q];
-            } else {
-              float v[8] = {lo[q][0], lo[q][1], lo[q][2], lo[q][3], hi[q][0], hi[q][1], hi[q][2], hi[q][3]};
-              finish(p, row * p.J + j0 + col, v, bias, x[q]);
-            }
-          }
+      for (int q = 0; q < NP; ++q) *reinterpret_cast<u32x4 *>(base + q * pass + 2 * o.off) = x[q];
+    } else {
+#pragma unroll
+      for (int q = 0; q < NP; ++q)
+        if (inside(o, tm, u, q)) *reinterpret_cast<u32x4 *>(base + q * pass + 2 * o.off) = x[q];
+    }
+  }
+
+  template <int U, bool ADD, bool ZX>
+  __device__ __forceinline__ void finish_unit(const Out &o, int tm, const Extras<ADD, ZX> &x) {
+    uint8_t *t;
+    if constexpr (WHOLE)
+      t = sm.out[w];
+    else
+      t = sm.a[0] + w * (32 * CH * 16);
+    const int lr = lane / LPR, c = lane % LPR;
+    put_unit<U>(tm, t);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    f32x4 v[NP][2];
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+      const int rr = q * RP + lr;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[q][h] = *reinterpret_cast<const f32x4 *>(t + 16 * (rr * CH + ((2 * c + h) ^ (rr & (CH - 1)))));
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (MODE == WGRAD || o.part) {
+      float *dst = o.part ? o.part + (32 * wm + 32 * WM * tm) * BN + 32 * TN * wn + 32 * UN * U : p.dw + o.first + unit_at(tm, U);
+      const int64_t ld = o.part ? BN : p.J;
+      uint8_t *base = const_cast<uint8_t *>(uniform(dst));
+      const uint32_t off = 4 * (o.part ? (uint32_t)(lr * BN + 8 * c) : o.off);
+#pragma unroll
+      for (int q = 0; q < NP; ++q) {
+        f32x4 *d = reinterpret_cast<f32x4 *>(base + q * (RP * ld * 4) + off);
+        if (o.whole || inside(o, tm, U, q)) {
+          if (MODE == WGRAD && p.accumulate && !o.part) v[q][0] += d[0], v[q][1] += d[1];
+          d[0] = v[q][0];
+          d[1] = v[q][1];
         }
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      return;
     }
-    barrier_lds();  // the stages are free for the next tile
+    auto each = [&](auto f) {
+#pragma unroll
+      for (int q = 0; q < NP; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[q][i >> 2][i & 3] = f(q, i, v[q][i >> 2][i & 3]);
+    };
+    u32x4 r[NP];
+    auto packed = [&] {
+#pragma unroll
+      for (int q = 0; q < NP; ++q) {
+        const float f[8] = {v[q][0][0], v[q][0][1], v[q][0][2], v[q][0][3], v[q][1][0], v[q][1][1], v[q][1][2], v[q][1][3]};
+        r[q] = pack(f);
+      }
+    };
+    if constexpr (MODE == FWD) {
+      if (p.bias) {
+        const u32x4 b = load8(o.cols > 32 * UN * U ? o.bias + 32 * UN * U + 8 * c : p.bias);
+        each([&](int, int i, float f) { return f + unpack(b, i); });
+      }
+      if (p.z) {
+        packed();
+        store_rows(o, p.z, tm, U, r);
+      }
+      if (p.act == BQM_ACT_RELU)
+        each([](int, int, float f) { return act_f(BQM_ACT_RELU, f); });
+      else if (p.act == BQM_ACT_SILU)
+        each([](int, int, float f) { return act_f(BQM_ACT_SILU, f); });
+      else if (p.act == BQM_ACT_GELU_TANH)
+        each([](int, int, float f) { return act_f(BQM_ACT_GELU_TANH, f); });
+    } else if constexpr (ZX) {
+      if (p.act == BQM_ACT_RELU)
+        each([&](int q, int i, float f) { return f * act_grad_f(BQM_ACT_RELU, unpack(x.zx[q], i)); });
+      else if (p.act == BQM_ACT_SILU)
+        each([&](int q, int i, float f) { return f * act_grad_f(BQM_ACT_SILU, unpack(x.zx[q], i)); });
+      else
+        each([&](int q, int i, float f) { return f * act_grad_f(BQM_ACT_GELU_TANH, unpack(x.zx[q], i)); });
+    }
+    if constexpr (ADD) each([&](int q, int i, float f) { return f + unpack(x.add[q], i); });
+    packed();
+    store_rows(o, p.out, tm, U, r);
+  }
+
+  template <int VT, bool ADD, bool ZX>
+  __device__ __forceinline__ void store(const Out &o) {
+    Extras<ADD, ZX> x0, x1;
+    load_extras(o, 0, 0, x0);
+#pragma unroll 1
+    for (int tm = 0; tm < VT; ++tm) {
+      const int next = tm + 1 < VT ? tm + 1 : tm;
+      if constexpr (UC == 2) {
+        load_extras(o, tm, 1, x1);
+        finish_unit<0>(o, tm, x0);
+        load_extras(o, next, 0, x0);
+        finish_unit<1>(o, tm, x1);
+      } else {
+        load_extras(o, next, 0, x1);
+        finish_unit<0>(o, tm, x0);
+        x0 = x1;
+      }
+    }
+  }
+  template <int VT>
+  __device__ __forceinline__ void store(const Out &o) {
+    const bool add = MODE != WGRAD && !o.part && p.add, zx = MODE == DGRAD && !o.part && p.act != BQM_ACT_NONE;
+    constexpr bool A = MODE != WGRAD, Z = MODE == DGRAD;
+    if (add)
+      zx ? store<VT, A, Z>(o) : store<VT, A, false>(o);
+    else
+      zx ? store<VT, false, Z>(o) : store<VT, false, false>(o);
+  }
+  template <int VT>
+  __device__ __forceinline__ void run_and_store(const Out &o, int k0, int k1) {
+    run<VT>(k0, k1);
+    store<VT>(o);
   }
 
   __device__ __forceinline__ void tile(int L, int k0, int k1, float *part) {
@@ -484,36 +802,34 @@ struct Tile {
     const int64_t i0 = (int64_t)at.x * BM, j0 = (int64_t)at.y * BN;
     a.setup(p.a, p.lda, p.C, p.I, i0, lane, w);
     b.setup(p.b, p.ldb, p.C, p.J, j0, lane, w);
+    a.setup_fragments(32 * wm);
+    b.setup_fragments(32 * TN * wn);
     const int rows = (int)min(p.I - i0, (int64_t)BM), vt = (rows + 32 * WM - 1) / (32 * WM);
+    const Out o = out_of(i0, j0, part);
     if (TM == 4 && vt > 3)
-      run<TM>(k0, k1);
+      run_and_store<TM>(o, k0, k1);
     else if (TM == 4 && vt > 2)
-      run<TM == 4 ? 3 : TM>(k0, k1);
+      run_and_store<TM == 4 ? 3 : TM>(o, k0, k1);
     else if (TM >= 2 && vt > 1)
-      run<TM >= 2 ? 2 : TM>(k0, k1);
+      run_and_store<TM >= 2 ? 2 : TM>(o, k0, k1);
     else
-      run<1>(k0, k1);
-    store(vt, i0, j0, part);
+      run_and_store<1>(o, k0, k1);
+    // no copy of this tile lands, and no wave reads a stage, when the next tile's copies begin
+    wait_vm<0>();
+    barrier_lds();
   }
 
   static constexpr int GM = TM == 4 ? 4 : 8;
-  // row and column tile of tile L: groups of about G row tiles, column by column
-  template <int G>
-  __device__ __forceinline__ static int2 tile_at(const LinParams &p, int L) {
-    const int n_g = max((p.NI + G / 2) / G, 1), g = (p.NI + n_g - 1) / n_g;
-    const int m_first = L / (g * p.NJ) * g, gm = min(g, p.NI - m_first), in_g = L - m_first * p.NJ;
-    return make_int2(m_first + in_g % gm, in_g / gm);
-  }
 };
 
 // Workgroups b % 8 are one XCD: each walks a contiguous range of tiles, so that the tiles in
 // flight there share rows and columns in its L2.  First whole rounds of tiles, one for every
 // workgroup; the tiles left over are split along the contraction into S parts, whose FP32 sums
 // go to part and are joined by join_parts.
-template <int WM, int TM, int TN, bool AT, bool BT, bool FAST, int OCC, int NS>
+template <int WM, int TM, int TN, bool AT, bool BT, bool FAST, int OCC, int NSA, int NSB>
 __global__ void __launch_bounds__(NTHR, OCC) lin_tiles(LinParams p) {
-  using T = Tile<WM, TM, TN, AT, BT, FAST, NS>;
-  __shared__ __attribute__((aligned(16))) Smem<T::BM, T::BN, NS> sm;
+  using T = Tile<WM, TM, TN, AT, BT, FAST, NSA, NSB>;
+  __shared__ __attribute__((aligned(16))) typename T::Mem sm;
   T t(p, sm);
   const int x = blockIdx.x & 7, q = blockIdx.x >> 3, nq = gridDim.x >> 3;
   const int full8 = p.full / 8, items = p.rem * p.S, per8 = (items + 7) / 8;
@@ -527,7 +843,8 @@ __global__ void __launch_bounds__(NTHR, OCC) lin_tiles(LinParams p) {
     }
     const bool split = L >= full8 && p.S > 1;
     const int k0 = split ? s * p.per : 0, k1 = split ? min(k0 + p.per, p.nk) : p.nk;
-    t.tile(tile, k0, k1, split ? p.part + ((int64_t)(tile - p.full) * p.S + s) * (T::BM * T::BN) : nullptr);
+    // (in scalar registers: the divisions that they come from are done in vector ones)
+    t.tile(__builtin_amdgcn_readfirstlane(tile), __builtin_amdgcn_readfirstlane(k0), __builtin_amdgcn_readfirstlane(k1), split ? p.part + ((int64_t)(tile - p.full) * p.S + s) * (T::BM * T::BN) : nullptr);
   }
 }
 #undef LIN_PIN
@@ -539,7 +856,7 @@ __global__ void __launch_bounds__(256) join_parts(LinParams p) {
   const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int r = (int)(n / U), u = (int)(n % U);
   if (r >= p.rem) return;
-  const int2 at = Tile<2, BM / 64, BN / 64, false, false, true, 2>::template tile_at<GM>(p, p.full + r);
+  const int2 at = tile_at<GM>(p, p.full + r);
   const int64_t row = (int64_t)at.x * BM + u / UR, col = (int64_t)at.y * BN + 8 * (u % UR);
   if (row >= p.I || col >= p.J) return;
   const float *q = p.part + (int64_t)r * p.S * (BM * BN) + 8 * u;
@@ -554,6 +871,79 @@ __global__ void __launch_bounds__(256) join_parts(LinParams p) {
   }
   float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   finish(p, row * p.J + col, v, bias, x);
+}
+
+// ---------------------------------------------------------------------------
+// the forward of few rows
+// ---------------------------------------------------------------------------
+// A few rows of x: the weights' bytes bound it, each of which is read once.  A workgroup takes
+// 16 rows of w, each of its FW waves every FW-th group of 128 of the contraction, straight from
+// memory into the operands of the 16x16x32 MFMA (lane l: row l % 16, elements 8 (l / 16) + 0..7
+// of 32; rows of x past the last are the last again), with the next group's loads in flight.
+// Weights are the first operand, so lane l ends with columns 4 (l / 16) + 0..3 of row l % 16 of
+// the result.  The waves' sums are added in their order through LDS.
+constexpr int kFewRows = 4;
+constexpr int FW = 8, FU = 4;  // waves; MFMA steps of 32 per group
+
+__global__ void __launch_bounds__(64 * FW) lin_few(LinParams p) {
+  __shared__ float sum[FW][16][20];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int K = p.C, M = (int)p.I, N = (int)p.J, n0 = blockIdx.x * 16;
+  const int e = 8 * (lane >> 4);
+  const uint8_t *wr = p.b + (int64_t)min(n0 + (lane & 15), N - 1) * p.ldb;
+  const uint8_t *xr = p.a + (int64_t)min(lane & 15, M - 1) * p.lda;
+  f32x4 acc = {};
+  u32x4 wf[2][FU], xf[2][FU];
+  // group i into set b; what lies past the end of the rows is their last 8 elements again,
+  // and zeros before it is used
+  auto load = [&](int b, int i) {
+#pragma unroll
+    for (int u = 0; u < FU; ++u) {
+      const int k = 2 * min(32 * (FU * i + u) + e, K - 8);
+      wf[b][u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wr + k));
+      xf[b][u] = *reinterpret_cast<const u32x4 *>(xr + k);
+    }
+  };
+  auto use = [&](int b, int i) {
+    if (32 * FU * (i + 1) > K) {
+#pragma unroll
+      for (int u = 0; u < FU; ++u) {
+        const uint32_t in = 32 * (FU * i + u) + e < K ? ~0u : 0u;
+        wf[b][u] &= u32x4{in, in, in, in};
+        xf[b][u] &= u32x4{in, in, in, in};
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < FU; ++u)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wf[b][u]), __builtin_bit_cast(bf16x8, xf[b][u]),
+                                                    acc, 0, 0, 0);
+  };
+  const int groups = (K + 32 * FU - 1) / (32 * FU);
+  if (w < groups) load(0, w);
+  for (int i = w; i < groups; i += 2 * FW) {
+    if (i + FW < groups) load(1, i + FW);
+    use(0, i);
+    if (i + FW < groups) {
+      if (i + 2 * FW < groups) load(0, i + 2 * FW);
+      use(1, i + FW);
+    }
+  }
+  *reinterpret_cast<f32x4 *>(&sum[w][lane & 15][4 * (lane >> 4)]) = acc;
+  __syncthreads();
+  if ((int)threadIdx.x < 2 * M) {
+    const int row = threadIdx.x >> 1, c = 8 * (threadIdx.x & 1), col = n0 + c;
+    if (col >= N) return;
+    const int64_t at = (int64_t)row * N + col;
+    u32x4 bias = {};
+    if (p.bias) bias = load8(p.bias + col);
+    const Extra x = load_extra(p, at);
+    float v[8] = {};
+#pragma unroll
+    for (int q = 0; q < FW; ++q)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += sum[q][row][c + i];
+    finish(p, at, v, bias, x);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -640,9 +1030,13 @@ bqm_status check_linear(const char *who, int64_t M, int64_t N, int64_t K) {
 // with every workgroup slot busy)
 struct Shape {
   int bm, bn, occ;
-  float step, rest;
+  float step, rest;    // us
+  float step2, rest2;  // with two workgroups per CU
 };
-constexpr Shape kShapes[3] = {{256, 256, 1, 1000, 8000}, {128, 128, 2, 800, 4000}, {64, 128, 3, 800, 4000}};
+constexpr Shape kShapes[4] = {{256, 256, 1, 1.0f, 12.4f, 0, 0}, {256, 128, 1, .53f, 8.6f, 0, 0},
+                              {128, 128, 1, .42f, 7.0f, 0, 0}, {64, 64, 2, .19f, 5.7f, .60f, 4.5f}};
+constexpr float kJoin = 4.6f, kJoinRate = 7.5e6f;  // us of a join's launch; its bytes per us
+constexpr int kSlow = 2;  // the shape for contractions of less than a step
 
 struct Plan {
   int shape, NI, NJ, full, rem, S, per, nk;
@@ -652,22 +1046,24 @@ struct Plan {
 Plan plan_of(int64_t I, int64_t J, int64_t C) {
   Plan best = {};
   float least = 0.0f;
-  const int nk = (int)cdiv(C, KS);
-  for (int h = 0; h < 3; ++h) {
+  for (int h = 0; h < 4; ++h) {
     const Shape &s = kShapes[h];
-    if (C < KS && h != 1) continue;
-    const int64_t NI = cdiv(I, s.bm), NJ = cdiv(J, s.bn), slots = kCUs * s.occ;
-    const int64_t full = NI * NJ / slots * slots, rem = NI * NJ - full;
-    for (int S = 1; S <= (rem ? 32 : 1); ++S) {
-      if (S > 1 && (rem * S > slots || cdiv(nk, S) < 2)) break;
+    if (C < 64 && h != kSlow) continue;
+    const int64_t tiles = cdiv(I, s.bm) * cdiv(J, s.bn);
+    const int nk = (int)cdiv(C, KS);
+    for (int S = 1; S <= 32; ++S) {
+      const bool two = s.occ == 2 && tiles * S > kCUs;
+      const int64_t slots = two ? 2 * kCUs : kCUs, full = tiles / slots * slots, rem = tiles - full;
       const int per = (int)cdiv(nk, S);
+      if (S > 1 && (rem == 0 || rem * S > slots || per < 2)) break;
       if (S > 1 && (int64_t)per * (S - 1) >= nk) continue;  // a part without steps
-      float t = full / slots * (nk * s.step + s.rest);
-      if (rem) t += per * s.step + s.rest;
-      if (S > 1) t += 5000.0f + 2.0f * rem * S * s.bm * s.bn * 4 / 4000.0f;  // a launch; 4 TB/s
+      const float step = two ? s.step2 : s.step, rest = two ? s.rest2 : s.rest;
+      float t = full / slots * (nk * step + rest);
+      if (rem) t += per * step + rest;
+      if (S > 1) t += kJoin + 8.0f * rem * S * s.bm * s.bn / kJoinRate;  // written and read
       if (least == 0.0f || t < least) {
         least = t;
-        best = {h, (int)NI, (int)NJ, (int)full, (int)rem, S, per, nk, S > 1 ? rem * S * s.bm * s.bn : 0};
+        best = {h, (int)cdiv(I, s.bm), (int)cdiv(J, s.bn), (int)full, (int)rem, S, per, nk, S > 1 ? rem * S * s.bm * s.bn : 0};
       }
     }
   }
@@ -693,25 +1089,30 @@ template <bool AT, bool BT>
 bqm_status launch_tiles(LinParams p, const Plan &plan, hipStream_t s, const char *what) {
   p.NI = plan.NI, p.NJ = plan.NJ, p.full = plan.full, p.rem = plan.rem, p.S = plan.S, p.per = plan.per, p.nk = plan.nk;
   const Shape &h = kShapes[plan.shape];
-  const int64_t slots = kCUs * h.occ, items = plan.full ? slots : (int64_t)plan.rem * plan.S;
-  const unsigned grid = (unsigned)(cdiv(items < slots ? items : slots, 8) * 8);
-  if (p.C < KS)
-    lin_tiles<2, 2, 2, AT, BT, false, 2, 2><<<grid, NTHR, 0, s>>>(p);
+  const int64_t slots = kCUs * h.occ, tiles = (int64_t)plan.full + (int64_t)plan.rem * plan.S;
+  const unsigned grid = (unsigned)(cdiv(tiles < slots ? tiles : slots, 8) * 8);
+  const unsigned joins = (unsigned)cdiv((int64_t)plan.rem * h.bm * h.bn / 8, 256);
+  auto go = [&](auto WM, auto TM, auto TN, auto FAST, auto OCC, auto NSA, auto NSB) {
+    lin_tiles<WM.value, TM.value, TN.value, AT, BT, FAST.value, OCC.value, NSA.value, NSB.value><<<grid, NTHR, 0, s>>>(p);
+    if (plan.S > 1)
+      join_parts<32 * WM.value * TM.value, 32 * (4 / WM.value) * TN.value, TM.value == 4 ? 4 : 8><<<joins, 256, 0, s>>>(p);
+  };
+  constexpr std::integral_constant<int, 1> n1;
+  constexpr std::integral_constant<int, 2> n2;
+  constexpr std::integral_constant<int, 3> n3;
+  constexpr std::integral_constant<int, 4> n4;
+  constexpr std::true_type fast;
+  constexpr std::false_type slow;
+  if (p.C < 64)
+    go(n2, n2, n2, slow, n1, n4, n4);
   else if (plan.shape == 0)
-    lin_tiles<2, 4, 4, AT, BT, true, 1, 2><<<grid, NTHR, 0, s>>>(p);
+    go(n2, n4, n4, fast, n1, n3, n2);
   else if (plan.shape == 1)
-    lin_tiles<2, 2, 2, AT, BT, true, 2, 2><<<grid, NTHR, 0, s>>>(p);
+    go(n2, n4, n2, fast, n1, n3, n3);
+  else if (plan.shape == 2)
+    go(n2, n2, n2, fast, n1, n4, n4);
   else
-    lin_tiles<2, 1, 2, AT, BT, true, 3, 2><<<grid, NTHR, 0, s>>>(p);
-  if (plan.S > 1) {
-    const unsigned n = (unsigned)cdiv((int64_t)plan.rem * h.bm * h.bn / 8, 256);
-    if (plan.shape == 0)
-      join_parts<256, 256, 4><<<n, 256, 0, s>>>(p);
-    else if (plan.shape == 1)
-      join_parts<128, 128, 8><<<n, 256, 0, s>>>(p);
-    else
-      join_parts<64, 128, 8><<<n, 256, 0, s>>>(p);
-  }
+    go(n2, n1, n1, fast, n2, n4, n4);
   return launch_status(what);
 }
 
@@ -735,7 +1136,7 @@ using namespace bqm;
 
 extern "C" size_t bqm_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (check_linear("bqm_linear_workspace_size", M, N, K) != BQM_OK || M == 0) return 0;
-  int64_t most = plan_of(M, N, K).part;
+  int64_t most = M <= kFewRows ? 0 : plan_of(M, N, K).part;
   const int64_t d = plan_of(M, K, N).part, w = wgrad_floats(M, N, K);
   most = d > most ? d : most;
   return ws_size(w > most ? w : most);
@@ -751,7 +1152,8 @@ extern "C" bqm_status bqm_linear_fwd(const uint16_t *x, const uint16_t *w, const
   BQM_REQUIRE(x && w && y, BQM_ERR_INVALID_ARG, "%s: x, w or y is NULL", who);
   BQM_REQUIRE(aligned16(x) && aligned16(w) && aligned16(bias) && aligned16(residual) && aligned16(y) && aligned16(z),
               BQM_ERR_ALIGN, "%s: pointer not 16-byte aligned", who);
-  const Plan plan = plan_of(M, N, K);
+  const bool few = M <= kFewRows;
+  const Plan plan = few ? Plan{} : plan_of(M, N, K);
   st = check_ws(who, ws, ws_bytes, (size_t)plan.part * 4);
   if (st != BQM_OK) return st;
   LinParams p = {};
@@ -760,6 +1162,10 @@ extern "C" bqm_status bqm_linear_fwd(const uint16_t *x, const uint16_t *w, const
   p.b = reinterpret_cast<const uint8_t *>(w), p.ldb = 2 * K, p.J = N;
   p.C = (int)K;
   p.bias = bias, p.add = residual, p.out = y, p.z = z, p.part = reinterpret_cast<float *>(ws);
+  if (few) {
+    lin_few<<<(unsigned)cdiv(N, 16), 64 * FW, 0, as_stream(stream)>>>(p);
+    return launch_status(who);
+  }
   return launch_tiles<false, false>(p, plan, as_stream(stream), who);
 }
 
