@@ -9,8 +9,11 @@
 // All three go by tokens, so that a token's row is read or written once and only the k rows
 // of its pairs are spread: the bytes are the least there are, T H + R H (twice R H for the
 // gradient), and HBM bounds them.  A lane holds 8 consecutive elements (16-byte accesses;
-// one element where H is no multiple of 8) of the token and of up to 8 of its rows at a
-// time, all loaded before the first is used.
+// one element where H is no multiple of 8) of the token and of several of its rows at a
+// time, all loaded before the first is used.  The experts' rows are read, and all results
+// written, past the caches, the tokens' rows are read through them: 16384 x 8 x 6144, dispatch
+// 307 us (379 with everything past them, 366 with nothing), combine 309 (355, 392), gradient
+// 636 (680, 687), which are 5.9, 6.5 and 5.4 TB/s.
 #include "common.h"
 
 namespace bqm {
@@ -18,9 +21,12 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kGroup = 8;      // pairs in flight per lane
+// Pairs in flight per lane, G: 8 for up to kFewTokens tokens, where a load's latency counts, 4
+// for more, where the registers of 8 cost workgroups in flight (16384 x 2 x 768: combine 20.3
+// against 18.1 us, gradient 32.6 against 28.2; 16384 x 8 x 6144 the same within 1%).
+constexpr int64_t kFewTokens = 512;
 constexpr int kPacked = 32;    // units per row up to which a wave takes several tokens
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 1024;
 constexpr int64_t kMaxBlocks = 1 << 22;
 
 struct RowsParams {
@@ -43,7 +49,8 @@ struct Unit;
 template <>
 struct Unit<8> {
   u32x4 v;
-  __device__ __forceinline__ void load(const uint16_t *p) {
+  __device__ __forceinline__ void load(const uint16_t *p) { v = *reinterpret_cast<const u32x4 *>(p); }
+  __device__ __forceinline__ void load_once(const uint16_t *p) {
     v = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
   }
   __device__ __forceinline__ void store(uint16_t *p) const {
@@ -59,6 +66,7 @@ template <>
 struct Unit<1> {
   uint16_t v;
   __device__ __forceinline__ void load(const uint16_t *p) { v = *p; }
+  __device__ __forceinline__ void load_once(const uint16_t *p) { v = *p; }
   __device__ __forceinline__ void store(uint16_t *p) const { *p = v; }
   __device__ __forceinline__ float get(int) const { return __uint_as_float((uint32_t)v << 16); }
   __device__ __forceinline__ void set(const float *f) { v = (uint16_t)pack_bf16_rne(f[0], 0.0f); }
@@ -113,7 +121,7 @@ __global__ void __launch_bounds__(kMaxThreads) dispatch_rows(RowsParams p) {
   }
 }
 
-template <int V, bool PACKED>
+template <int V, bool PACKED, int G>
 __global__ void __launch_bounds__(kMaxThreads) combine_rows(RowsParams p) {
   const Place<PACKED> at(p);
   const int64_t live = live_rows(p);
@@ -124,20 +132,20 @@ __global__ void __launch_bounds__(kMaxThreads) combine_rows(RowsParams p) {
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-    for (int j0 = 0; j0 < p.k; j0 += kGroup) {
-      Unit<V> u[kGroup];
-      int64_t row[kGroup];
-      float w[kGroup];
+    for (int j0 = 0; j0 < p.k; j0 += G) {
+      Unit<V> u[G];
+      int64_t row[G];
+      float w[G];
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
+      for (int j = 0; j < G; ++j) {
         row[j] = place(p, at.t, j0 + j, live);
         w[j] = p.w && row[j] >= 0 ? p.w[at.t * p.k + j0 + j] : 1.0f;
       }
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j)
-        if (row[j] >= 0) u[j].load(p.y + (row[j] * p.upr + c) * V);
+      for (int j = 0; j < G; ++j)
+        if (row[j] >= 0) u[j].load_once(p.y + (row[j] * p.upr + c) * V);
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j)
+      for (int j = 0; j < G; ++j)
         if (row[j] >= 0) {
 #pragma unroll
           for (int i = 0; i < V; ++i) acc[i] += w[j] * u[j].get(i);
@@ -152,31 +160,31 @@ __global__ void __launch_bounds__(kMaxThreads) combine_rows(RowsParams p) {
   }
 }
 
-template <int V, bool PACKED>
+template <int V, bool PACKED, int G>
 __global__ void __launch_bounds__(kMaxThreads) combine_grad_rows(RowsParams p) {
-  __shared__ float part[kMaxThreads / 64][kGroup];
+  __shared__ float part[kMaxThreads / 64][G];
   const Place<PACKED> at(p);
   const int64_t live = live_rows(p);
-  for (int j0 = 0; j0 < p.k; j0 += kGroup) {
-    int64_t row[kGroup];
-    float w[kGroup], dot[kGroup];
+  for (int j0 = 0; j0 < p.k; j0 += G) {
+    int64_t row[G];
+    float w[G], dot[G];
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) {
+    for (int j = 0; j < G; ++j) {
       row[j] = at.t < p.T ? place(p, at.t, j0 + j, live) : -1;
       w[j] = p.w && row[j] >= 0 ? p.w[at.t * p.k + j0 + j] : 1.0f;
       dot[j] = 0.0f;
     }
     for (uint32_t c = at.c; c < at.end; c += at.step) {
-      Unit<V> d, u[kGroup];
+      Unit<V> d, u[G];
       d.load(p.x + (at.t * p.upr + c) * V);
       if (p.dw) {
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-          if (row[j] >= 0) u[j].load(p.y + (row[j] * p.upr + c) * V);
+        for (int j = 0; j < G; ++j)
+          if (row[j] >= 0) u[j].load_once(p.y + (row[j] * p.upr + c) * V);
       }
       if (p.out) {
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
+        for (int j = 0; j < G; ++j)
           if (row[j] >= 0) {
             float f[V];
 #pragma unroll
@@ -188,7 +196,7 @@ __global__ void __launch_bounds__(kMaxThreads) combine_grad_rows(RowsParams p) {
       }
       if (p.dw) {
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
+        for (int j = 0; j < G; ++j)
           if (row[j] >= 0) {
 #pragma unroll
             for (int i = 0; i < V; ++i) dot[j] += d.get(i) * u[j].get(i);
@@ -198,21 +206,21 @@ __global__ void __launch_bounds__(kMaxThreads) combine_grad_rows(RowsParams p) {
     if (!p.dw) continue;
     // the lanes' sums in a fixed butterfly, then the waves' in order
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j)
+    for (int j = 0; j < G; ++j)
       for (int m = PACKED ? 1 << p.logL >> 1 : 32; m >= 1; m >>= 1) dot[j] += __shfl_xor(dot[j], m, 64);
     if constexpr (PACKED) {
       if (at.t < p.T && at.c == 0) {
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
+        for (int j = 0; j < G; ++j)
           if (j0 + j < p.k) p.dw[at.t * p.k + j0 + j] = dot[j];
       }
     } else {
       if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) part[threadIdx.x >> 6][j] = dot[j];
+        for (int j = 0; j < G; ++j) part[threadIdx.x >> 6][j] = dot[j];
       }
       __syncthreads();
-      if (at.t < p.T && threadIdx.x < kGroup && j0 + (int)threadIdx.x < p.k) {
+      if (at.t < p.T && threadIdx.x < G && j0 + (int)threadIdx.x < p.k) {
         float s = 0.0f;
         for (unsigned q = 0; q < blockDim.x / 64; ++q) s += part[q][threadIdx.x];
         p.dw[at.t * p.k + j0 + threadIdx.x] = s;
@@ -267,13 +275,16 @@ void go(RowsParams &p, int64_t H, bool whole, Launch launch) {
 
 using namespace bqm;
 
-#define BQM_ROWS_LAUNCH(kernel)                                               \
-  [&](int V, bool packed, dim3 grid, dim3 block) {                            \
-    const hipStream_t s = as_stream(stream);                                  \
-    if (V == 8)                                                               \
-      packed ? kernel<8, true><<<grid, block, 0, s>>>(p) : kernel<8, false><<<grid, block, 0, s>>>(p); \
-    else                                                                      \
-      packed ? kernel<1, true><<<grid, block, 0, s>>>(p) : kernel<1, false><<<grid, block, 0, s>>>(p); \
+// kernel<V, PACKED, extra ..>
+#define BQM_ROWS_LAUNCH(kernel, ...)                                                    \
+  [&](int V, bool packed, dim3 grid, dim3 block) {                                      \
+    const hipStream_t s = as_stream(stream);                                            \
+    if (V == 8)                                                                         \
+      packed ? kernel<8, true, ##__VA_ARGS__><<<grid, block, 0, s>>>(p)                 \
+             : kernel<8, false, ##__VA_ARGS__><<<grid, block, 0, s>>>(p);               \
+    else                                                                                \
+      packed ? kernel<1, true, ##__VA_ARGS__><<<grid, block, 0, s>>>(p)                 \
+             : kernel<1, false, ##__VA_ARGS__><<<grid, block, 0, s>>>(p);               \
   }
 
 extern "C" bqm_status bqm_dispatch(const uint16_t *x, const int32_t *inv, int64_t T, int64_t H, int32_t k,
@@ -301,7 +312,10 @@ extern "C" bqm_status bqm_combine(const uint16_t *y, const int32_t *inv, const f
   BQM_REQUIRE(aligned4(n_rows), BQM_ERR_ALIGN, "%s: n_rows not 4-byte aligned", who);
   RowsParams p = {};
   p.x = residual, p.y = y, p.inv = inv, p.n_rows = n_rows, p.w = topk_w, p.out = out, p.T = T, p.R = T * k, p.k = k;
-  go(p, H, false, BQM_ROWS_LAUNCH(combine_rows));
+  if (T <= kFewTokens)
+    go(p, H, false, BQM_ROWS_LAUNCH(combine_rows, 8));
+  else
+    go(p, H, false, BQM_ROWS_LAUNCH(combine_rows, 4));
   return launch_status(who);
 }
 
@@ -320,7 +334,10 @@ extern "C" bqm_status bqm_combine_grad(const uint16_t *dout, const uint16_t *y, 
   RowsParams p = {};
   p.x = dout, p.y = y, p.inv = inv, p.n_rows = n_rows, p.w = topk_w, p.out = dy, p.dw = dtopk_w;
   p.T = T, p.R = T * k, p.k = k;
-  go(p, H, dtopk_w != nullptr, BQM_ROWS_LAUNCH(combine_grad_rows));
+  if (T <= kFewTokens)
+    go(p, H, dtopk_w != nullptr, BQM_ROWS_LAUNCH(combine_grad_rows, 8));
+  else
+    go(p, H, dtopk_w != nullptr, BQM_ROWS_LAUNCH(combine_grad_rows, 4));
   return launch_status(who);
 }
 #undef BQM_ROWS_LAUNCH
