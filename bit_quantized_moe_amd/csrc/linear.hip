@@ -41,6 +41,7 @@ struct LinParams {
   int NI, NJ;            // tiles
   int full, rem;         // tiles computed whole, and those behind them
   int S, per;            // which are split into S parts of per steps
+  int grid;              // workgroups that walk tiles
   int mode, act, accumulate;
   const uint16_t *bias, *add, *zx;
   uint16_t *out, *z;
@@ -822,16 +823,58 @@ struct Tile {
   static constexpr int GM = TM == 4 ? 4 : 8;
 };
 
+// ---------------------------------------------------------------------------
+// column sums (the bias gradient)
+// ---------------------------------------------------------------------------
+// Workgroup n sums rows [y rows, (y + 1) rows) of 64 columns, y = n / (N / 64): 8 lanes of 8
+// columns, 32 rows at a time; the 32 partial sums are added in order through LDS.  One part per
+// y, or the gradient itself where there is one.
+struct ColSums {
+  const uint16_t *dz;
+  int64_t M, N, rows;
+  float *out;
+  int accumulate;
+};
+__device__ __forceinline__ void col_sums(const ColSums &p, int n, float (*s)[65]) {
+  const int nx = (int)((p.N + 63) / 64), y = n / nx, x = n - y * nx;
+  const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const int64_t col = (int64_t)x * 64 + 8 * c;
+  const int64_t r0 = y * p.rows, r1 = min(r0 + p.rows, p.M);
+  float v[8] = {};
+  if (col < p.N) {
+#pragma unroll 8
+    for (int64_t r = r0 + g; r < r1; r += 32) {
+      const u32x4 d = load8(p.dz + r * p.N + col);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += unpack(d, i);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[g][8 * c + i] = v[i];
+  __syncthreads();
+  const int64_t at = (int64_t)x * 64 + threadIdx.x;
+  if (threadIdx.x < 64 && at < p.N) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t += s[i][threadIdx.x];
+    float *o = p.out + y * p.N + at;
+    *o = p.accumulate ? *o + t : t;
+  }
+}
+
 // Workgroups b % 8 are one XCD: each walks a contiguous range of tiles, so that the tiles in
 // flight there share rows and columns in its L2.  First whole rounds of tiles, one for every
 // workgroup; the tiles left over are split along the contraction into S parts, whose FP32 sums
-// go to part and are joined by join_parts.
+// go to part and are joined by join_parts.  Workgroups behind those of the tiles take the
+// column sums.
 template <int WM, int TM, int TN, bool AT, bool BT, bool FAST, int OCC, int NSA, int NSB>
-__global__ void __launch_bounds__(NTHR, OCC) lin_tiles(LinParams p) {
+__global__ void __launch_bounds__(NTHR, OCC) lin_tiles(LinParams p, ColSums cols) {
   using T = Tile<WM, TM, TN, AT, BT, FAST, NSA, NSB>;
   __shared__ __attribute__((aligned(16))) typename T::Mem sm;
+  static_assert(sizeof(sm) >= 32 * 65 * 4, "the column sums' LDS");
+  if (AT && BT && (int)blockIdx.x >= p.grid) return col_sums(cols, (int)blockIdx.x - p.grid, reinterpret_cast<float(*)[65]>(&sm));
   T t(p, sm);
-  const int x = blockIdx.x & 7, q = blockIdx.x >> 3, nq = gridDim.x >> 3;
+  const int x = blockIdx.x & 7, q = blockIdx.x >> 3, nq = p.grid >> 3;
   const int full8 = p.full / 8, items = p.rem * p.S, per8 = (items + 7) / 8;
   for (int L = q; L < full8 + per8; L += nq) {
     int tile = x * full8 + L, s = 0;
@@ -946,39 +989,6 @@ __global__ void __launch_bounds__(64 * FW) lin_few(LinParams p) {
   }
 }
 
-// ---------------------------------------------------------------------------
-// column sums (the bias gradient)
-// ---------------------------------------------------------------------------
-// A workgroup sums rows [y rows, (y + 1) rows) of 64 columns: 8 lanes of 8 columns, 32 rows at
-// a time; the 32 partial sums are added in order through LDS.  One part per workgroup, or the
-// gradient itself where there is one.
-__global__ void __launch_bounds__(256) col_sums(const uint16_t *dz, int64_t M, int64_t N, int64_t rows, float *out,
-                                                int accumulate) {
-  __shared__ float s[32][65];
-  const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
-  const int64_t col = (int64_t)blockIdx.x * 64 + 8 * c;
-  const int64_t r0 = (int64_t)blockIdx.y * rows, r1 = min(r0 + rows, M);
-  float v[8] = {};
-  if (col < N) {
-#pragma unroll 4
-    for (int64_t r = r0 + g; r < r1; r += 32) {
-      const u32x4 d = load8(dz + r * N + col);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += unpack(d, i);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s[g][8 * c + i] = v[i];
-  __syncthreads();
-  const int64_t n = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (threadIdx.x < 64 && n < N) {
-    float t = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) t += s[i][threadIdx.x];
-    float *o = out + (int64_t)blockIdx.y * N + n;
-    *o = accumulate ? *o + t : t;
-  }
-}
 __global__ void __launch_bounds__(256) join_cols(const float *part, int64_t N, int parts, float *out, int accumulate) {
   const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (n >= N) return;
@@ -1070,10 +1080,9 @@ Plan plan_of(int64_t I, int64_t J, int64_t C) {
   return best;
 }
 
-// row parts of the column sums
+// row parts of the column sums: of at least 1024 rows, which take no longer than the tiles beside them
 int col_parts(int64_t M, int64_t N) {
-  const int64_t most = 2048 / cdiv(N, 64), want = cdiv(M, 256);
-  const int64_t n = want < most ? want : most;
+  const int64_t most = 2048 / cdiv(N, 64), want = cdiv(M, 1024), n = want < most ? want : most;
   return (int)(n < 1 ? 1 : n);
 }
 
@@ -1086,14 +1095,15 @@ int64_t wgrad_floats(int64_t M, int64_t N, int64_t K) {
 size_t ws_size(int64_t floats) { return align256((size_t)floats * 4); }
 
 template <bool AT, bool BT>
-bqm_status launch_tiles(LinParams p, const Plan &plan, hipStream_t s, const char *what) {
+bqm_status launch_tiles(LinParams p, const Plan &plan, hipStream_t s, const char *what, const ColSums &cols = {}) {
   p.NI = plan.NI, p.NJ = plan.NJ, p.full = plan.full, p.rem = plan.rem, p.S = plan.S, p.per = plan.per, p.nk = plan.nk;
   const Shape &h = kShapes[plan.shape];
   const int64_t slots = kCUs * h.occ, tiles = (int64_t)plan.full + (int64_t)plan.rem * plan.S;
-  const unsigned grid = (unsigned)(cdiv(tiles < slots ? tiles : slots, 8) * 8);
+  p.grid = (int)(cdiv(tiles < slots ? tiles : slots, 8) * 8);
+  const unsigned grid = (unsigned)(p.grid + (cols.out ? cdiv(cols.N, 64) * cdiv(cols.M, cols.rows) : 0));
   const unsigned joins = (unsigned)cdiv((int64_t)plan.rem * h.bm * h.bn / 8, 256);
   auto go = [&](auto WM, auto TM, auto TN, auto FAST, auto OCC, auto NSA, auto NSB) {
-    lin_tiles<WM.value, TM.value, TN.value, AT, BT, FAST.value, OCC.value, NSA.value, NSB.value><<<grid, NTHR, 0, s>>>(p);
+    lin_tiles<WM.value, TM.value, TN.value, AT, BT, FAST.value, OCC.value, NSA.value, NSB.value><<<grid, NTHR, 0, s>>>(p, cols);
     if (plan.S > 1)
       join_parts<32 * WM.value * TM.value, 32 * (4 / WM.value) * TN.value, TM.value == 4 ? 4 : 8><<<joins, 256, 0, s>>>(p);
   };
@@ -1218,12 +1228,11 @@ extern "C" bqm_status bqm_linear_wgrad(const uint16_t *dz, const uint16_t *x, in
   p.b = reinterpret_cast<const uint8_t *>(x), p.ldb = 2 * K, p.J = K;
   p.C = (int)M;
   p.dw = dw, p.part = reinterpret_cast<float *>(ws);
-  st = launch_tiles<true, true>(p, plan, s, who);
-  if (st != BQM_OK || !dbias) return st;
-  float *cols = parts > 1 ? p.part + plan.part : dbias;
-  const dim3 grid((unsigned)cdiv(N, 64), (unsigned)parts);
-  col_sums<<<grid, 256, 0, s>>>(dz, M, N, cdiv(M, parts), cols, parts == 1 && p.accumulate);
-  if (parts > 1) join_cols<<<(unsigned)cdiv(N, 256), 256, 0, s>>>(cols, N, parts, dbias, p.accumulate);
+  ColSums cols = {};
+  if (dbias) cols = {dz, M, N, cdiv(M, parts), parts > 1 ? p.part + plan.part : dbias, parts == 1 && p.accumulate};
+  st = launch_tiles<true, true>(p, plan, s, who, cols);
+  if (st != BQM_OK || parts == 1) return st;
+  join_cols<<<(unsigned)cdiv(N, 256), 256, 0, s>>>(cols.out, N, (int)cdiv(M, cols.rows), dbias, p.accumulate);
   return launch_status(who);
 }
 
