@@ -1026,7 +1026,8 @@ __global__ void __launch_bounds__(256) act_grad_rows(const uint16_t *dy, const u
 // ---------------------------------------------------------------------------
 bqm_status check_linear(const char *who, int64_t M, int64_t N, int64_t K) {
   BQM_REQUIRE(M >= 0, BQM_ERR_INVALID_ARG, "%s: M < 0", who);
-  BQM_REQUIRE(M < ((int64_t)1 << 31), BQM_ERR_SHAPE, "%s: M=%lld reaches 2^31", who, (long long)M);
+  // (the weight gradient counts rows, rounded up to steps, in 32 bits)
+  BQM_REQUIRE(M < ((int64_t)1 << 30), BQM_ERR_SHAPE, "%s: M=%lld reaches 2^30", who, (long long)M);
   BQM_REQUIRE(N >= 8 && N % 8 == 0 && N < (1 << 22), BQM_ERR_SHAPE, "%s: N=%lld is not a multiple of 8 in [8, 2^22)", who,
               (long long)N);
   BQM_REQUIRE(K >= 8 && K % 8 == 0 && K < (1 << 22), BQM_ERR_SHAPE, "%s: K=%lld is not a multiple of 8 in [8, 2^22)", who,
@@ -1243,7 +1244,8 @@ extern "C" bqm_status bqm_act_grad(const uint16_t *dy, const uint16_t *z, int32_
   if (st != BQM_OK) return st;
   BQM_REQUIRE(n >= 0, BQM_ERR_INVALID_ARG, "%s: n < 0", who);
   BQM_REQUIRE(act != BQM_ACT_NONE, BQM_ERR_INVALID_ARG, "%s: BQM_ACT_NONE has no gradient to apply", who);
-  BQM_REQUIRE(n < ((int64_t)1 << 35), BQM_ERR_SHAPE, "%s: n reaches 2^35", who);
+  // (a launch takes less than 2^32 threads, of 8 elements each)
+  BQM_REQUIRE(n < ((int64_t)1 << 34), BQM_ERR_SHAPE, "%s: n reaches 2^34", who);
   if (n == 0) return BQM_OK;
   BQM_REQUIRE(dy && z && dz, BQM_ERR_INVALID_ARG, "%s: dy, z or dz is NULL", who);
   BQM_REQUIRE(aligned16(dy) && aligned16(z) && aligned16(dz), BQM_ERR_ALIGN, "%s: pointer not 16-byte aligned", who);

@@ -27,7 +27,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int64_t kFewTokens = 512;
 constexpr int kPacked = 32;    // units per row up to which a wave takes several tokens
 constexpr int kMaxThreads = 1024;
-constexpr int64_t kMaxBlocks = 1 << 22;
+constexpr int64_t kMaxBlocks = 1 << 21;  // of kMaxThreads: a launch takes less than 2^32 threads in x
 
 struct RowsParams {
   const uint16_t *x;  // dispatch: x; combine: residual or NULL; gradient: dout
@@ -264,7 +264,6 @@ void go(RowsParams &p, int64_t H, bool whole, Launch launch) {
     block.x = (unsigned)(cdiv(cdiv(p.span, turns), 64) * 64);
     grid.y = parts;
   }
-  // a launch has less than 2^32 threads in x
   grid.x = (unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks);
   grid.z = (unsigned)cdiv(blocks, kMaxBlocks);
   launch(V, packed, grid, block);

@@ -328,7 +328,7 @@ bqm_status bqm_combine_grad(const uint16_t *dout, const uint16_t *y, const int32
 
 /* ---------------------------------------------------------------------------
  * The dense product that stands beside the routed experts (a shared expert, a dense layer):
- * bf16 weights w [N, K], M rows.  M >= 0; N and K multiples of 8 in [8, 2^22); M < 2^31.
+ * bf16 weights w [N, K], M rows.  0 <= M < 2^30; N and K multiples of 8 in [8, 2^22).
  * Products are exact in FP32, sums FP32; each output is rounded once.
  *
  * act: with s(v) = 1 / (1 + e^-v),
@@ -363,7 +363,7 @@ bqm_status bqm_linear_dgrad(const uint16_t *dz, const uint16_t *w, const uint16_
 bqm_status bqm_linear_wgrad(const uint16_t *dz, const uint16_t *x, int32_t accumulate, int64_t M, int64_t N, int64_t K,
                             float *dw, float *dbias, void *ws, size_t ws_bytes, void *stream);
 
-/* dz = dy act'(z) over n elements (bf16), where the activation is a layer's last step; dz may
+/* dz = dy act'(z) over n < 2^34 elements (bf16), where the activation is a layer's last step; dz may
  * be dy or z. */
 bqm_status bqm_act_grad(const uint16_t *dy, const uint16_t *z, int32_t act, int64_t n, uint16_t *dz, void *stream);
 

@@ -235,6 +235,31 @@ def test_past_four_gigabytes():
     assert ((dw.double() - ref).abs() <= M * F23 * mag).all()
 
 
+def test_most_rows():
+    """2^30 - 1 rows, nearly all zeros: whole numbers, exact in any order."""
+    import torch
+    log("most rows")
+    b = _bqm()
+    M, N, K = (1 << 30) - 1, 8, 8
+    g = torch.Generator(device=gpu()).manual_seed(2)
+    at = torch.cat([torch.randint(0, M, (4000,), generator=g, device=gpu()), torch.tensor([0, M - 70, M - 64, M - 1], device=gpu())]).unique()
+    some = lambda: torch.randint(-3, 4, (len(at), 8), generator=g, device=gpu()).bfloat16()  # noqa: E731
+    x, dz = (torch.zeros((M, 8), dtype=torch.bfloat16, device=gpu()) for _ in range(2))
+    x[at], dz[at] = some(), some()
+    w = some()[:8].contiguous()
+    ws = workspace(M, N, K)
+    X, D = x[at].double(), dz[at].double()
+    dw, db = empty(N, K, dtype=torch.float32), empty(N, dtype=torch.float32)
+    b.bqm_linear_wgrad(dz, x, dw, dbias=db, ws=ws)
+    assert torch.equal(dw.double(), D.T @ X) and torch.equal(db.double(), D.sum(0))
+    for product, a, ref in ((b.bqm_linear_fwd, x, X @ w.double().T), (b.bqm_linear_dgrad, dz, D @ w.double())):
+        out = product(a, w, torch.full_like(x, 5.0), ws=ws)
+        assert torch.equal(out[at].double(), ref)
+        out[at] = 0
+        assert not out.any()
+        del out
+
+
 def test_infinities_of_the_last_step():
     """Where the last step overlaps the one before, an infinity is counted once (0 times it
     would be NaN)."""

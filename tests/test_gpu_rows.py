@@ -209,13 +209,14 @@ def test_rows_past_four_gigabytes():
 
 
 def test_many_short_rows():
-    """More than 2^22 workgroups' worth of tokens (the grid's third dimension)."""
+    """More workgroups than the grid's first dimension takes, of one wave, of several tokens, and
+    of the most threads."""
     import torch
     log("many tokens")
     b = _bqm()
-    for T, k, H in (((1 << 22) + 5, 1, 264), ((1 << 26) + 37, 1, 16)):
+    for T, H, values in (((1 << 22) + 5, 264, 251), ((1 << 26) + 37, 16, 251), ((1 << 22) + 5, 1009, 128)):
         inv = torch.arange(T - 1, -1, -1, dtype=torch.int32, device=gpu())
-        x = (torch.arange(T, device=gpu(), dtype=torch.int32) % 251).to(torch.bfloat16).unsqueeze(1).expand(T, H).contiguous()
+        x = (torch.arange(T, device=gpu(), dtype=torch.int32) % values).to(torch.bfloat16).unsqueeze(1).expand(T, H).contiguous()
         rows = b.bqm_dispatch(x, inv, torch.zeros_like(x))
         assert torch.equal(rows, x.flip(0))
         assert torch.equal(b.bqm_combine(rows, inv, torch.zeros_like(x)), x)

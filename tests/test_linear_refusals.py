@@ -12,10 +12,10 @@ def lib():
 
 
 def sizes(f):
-    assert f(M=-1) == -1 and f(M=1 << 31) == -2
+    assert f(M=-1) == -1 and f(M=1 << 30) == -2 and f(M=1 << 31) == -2
     assert f(N=0) == -2 and f(N=12) == -2 and f(N=-8) == -2 and f(N=1 << 22) == -2
     assert f(K=0) == -2 and f(K=4) == -2 and f(K=1 << 22) == -2 and "K=" in bqm.bqm_last_error()
-    assert f(M=(1 << 31) - 1, N=(1 << 22) - 8) == -2 and "tiles" in bqm.bqm_last_error()
+    assert f(M=(1 << 30) - 1, N=(1 << 22) - 8) == -2 and "tiles" in bqm.bqm_last_error()
 
 
 def test_forward(lib):
@@ -56,7 +56,7 @@ def test_act_grad(lib):
     def f(dy=16, z=16, act=2, n=64, dz=16):
         return lib.bqm_act_grad(dy, z, act, n, dz, None)
     assert f(act=0) == -1 and f(act=4) == -1 and f(act=-2) == -1
-    assert f(n=-1) == -1 and f(n=1 << 35) == -2
+    assert f(n=-1) == -1 and f(n=1 << 34) == -2
     assert f(dy=None) == -1 and f(z=None) == -1 and f(dz=None) == -1
     assert f(dy=8) == -3 and f(z=8) == -3 and f(dz=8) == -3
     assert f(n=0, dy=None, z=None, dz=None) == 0
