@@ -57,21 +57,24 @@ __device__ __forceinline__ float sigmoid_f(float x) { return __builtin_amdgcn_rc
 constexpr float kGelu = 1.5957691216057308f;  // 2 sqrt(2/pi)
 
 __device__ __forceinline__ float act_f(int act, float v) {
-  if (act == BQM_ACT_RELU) return v > 0.0f ? v : 0.0f;
+  if (act == BQM_ACT_RELU) return v < 0.0f ? 0.0f : v;  // NaN stays
   if (act == BQM_ACT_SILU) return v * sigmoid_f(v);
   return v * sigmoid_f(kGelu * (v + 0.044715f * v * v * v));
 }
 
-__device__ __forceinline__ float act_grad_f(int act, float v) {
-  if (act == BQM_ACT_RELU) return v > 0.0f ? 1.0f : 0.0f;
+// d act'(v).  ReLU chooses: where it is off, nothing of d passes, NaN or infinite as it may be;
+// a NaN in v does not hide (d passes).
+__device__ __forceinline__ float through_act(int act, float d, float v) {
+  if (act == BQM_ACT_RELU) return v <= 0.0f ? 0.0f : d;
   if (act == BQM_ACT_SILU) {
     const float s = sigmoid_f(v);
-    return s * (1.0f + v * (1.0f - s));
+    return d * (s * (1.0f + v * (1.0f - s)));
   }
-  // past |v| = 16 the sigmoid is 0 or 1 in FP32 and so is the derivative; v^2 need not be formed
-  const float t = fminf(fmaxf(v, -16.0f), 16.0f), q = t * t;
+  // past |v| = 16 the sigmoid is 0 or 1 in FP32 and so is the derivative; v^2 need not be formed.
+  // Comparisons, as the minimum and maximum of the machine would make a number of a NaN.
+  const float t = v > 16.0f ? 16.0f : v < -16.0f ? -16.0f : v, q = t * t;
   const float s = sigmoid_f(kGelu * t * (1.0f + 0.044715f * q));
-  return s * (1.0f + t * (1.0f - s) * kGelu * (1.0f + 0.134145f * q));
+  return d * (s * (1.0f + t * (1.0f - s) * kGelu * (1.0f + 0.134145f * q)));
 }
 
 // ---------------------------------------------------------------------------
@@ -115,7 +118,7 @@ __device__ __forceinline__ void finish(const LinParams &p, int64_t at, float *v,
     }
   } else if (p.act != BQM_ACT_NONE) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= act_grad_f(p.act, unpack(x.zx, i));
+    for (int i = 0; i < 8; ++i) v[i] = through_act(p.act, v[i], unpack(x.zx, i));
   }
   if (p.add) {
 #pragma unroll
@@ -750,11 +753,11 @@ struct Tile {
         each([](int, int, float f) { return act_f(BQM_ACT_GELU_TANH, f); });
     } else if constexpr (ZX) {
       if (p.act == BQM_ACT_RELU)
-        each([&](int q, int i, float f) { return f * act_grad_f(BQM_ACT_RELU, unpack(x.zx[q], i)); });
+        each([&](int q, int i, float f) { return through_act(BQM_ACT_RELU, f, unpack(x.zx[q], i)); });
       else if (p.act == BQM_ACT_SILU)
-        each([&](int q, int i, float f) { return f * act_grad_f(BQM_ACT_SILU, unpack(x.zx[q], i)); });
+        each([&](int q, int i, float f) { return through_act(BQM_ACT_SILU, f, unpack(x.zx[q], i)); });
       else
-        each([&](int q, int i, float f) { return f * act_grad_f(BQM_ACT_GELU_TANH, unpack(x.zx[q], i)); });
+        each([&](int q, int i, float f) { return through_act(BQM_ACT_GELU_TANH, f, unpack(x.zx[q], i)); });
     }
     if constexpr (ADD) each([&](int q, int i, float f) { return f + unpack(x.add[q], i); });
     packed();
@@ -1013,11 +1016,11 @@ __global__ void __launch_bounds__(256) act_grad_rows(const uint16_t *dy, const u
     const u32x4 q = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(z + i));
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = unpack(d, j) * act_grad_f(act, unpack(q, j));
+    for (int j = 0; j < 8; ++j) v[j] = through_act(act, unpack(d, j), unpack(q, j));
     __builtin_nontemporal_store(pack(v), reinterpret_cast<u32x4 *>(dz + i));
   } else {
     for (int64_t j = i; j < n; ++j)
-      dz[j] = (uint16_t)pack_bf16_rne(bf16_lo(dy[j]) * act_grad_f(act, bf16_lo(z[j])), 0.0f);
+      dz[j] = (uint16_t)pack_bf16_rne(through_act(act, bf16_lo(dy[j]), bf16_lo(z[j])), 0.0f);
   }
 }
 

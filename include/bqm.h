@@ -334,7 +334,8 @@ bqm_status bqm_combine_grad(const uint16_t *dout, const uint16_t *y, const int32
  * act: with s(v) = 1 / (1 + e^-v),
  *   BQM_ACT_SILU       v s(v)
  *   BQM_ACT_GELU_TANH  v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2
- *   BQM_ACT_RELU       max(v, 0), whose derivative at 0 is taken as 0
+ *   BQM_ACT_RELU       max(v, 0); of a gradient nothing passes where v <= 0
+ * A NaN in v is a NaN in act(v) and in the gradient through it (ReLU: the gradient passes).
  *
  * ws: bqm_linear_workspace_size() bytes of device scratch, for partial sums where the
  * contraction is split over workgroups (0 bytes, and NULL, where no direction needs any); the

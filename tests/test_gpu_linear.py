@@ -352,6 +352,35 @@ def test_activations_far_from_zero():
     assert torch.isfinite(x).all()
 
 
+@pytest.mark.parametrize("name", ACTS[1:])
+def test_nan_and_infinity_through_activations(name):
+    """A NaN pre-activation shows in the output and in the gradient; infinities have the limits'
+    values where FP32 forms them; ReLU's gradient passes nothing where it is off."""
+    import torch
+    log(f"NaN and infinity {name}")
+    b = _bqm()
+    a, nan, inf = act_id(name), float("nan"), float("inf")
+    for M in (2, 40):       # by the forward of few rows, and by tiles
+        x = torch.zeros((M, 64), device=gpu()).bfloat16()
+        w, bias = torch.ones((16, 64), device=gpu()).bfloat16(), torch.zeros(16, device=gpu()).bfloat16()
+        bias[3], bias[4], bias[5] = nan, inf, -3.0
+        y = b.bqm_linear_fwd(x, w, empty(M, 16), bias=bias, act=a, ws=workspace(M, 16, 64))
+        assert y[:, 3].isnan().all() and (y[:, 4] == inf).all() and not y[:, 5].isnan().any() and (y[:, 6:] == 0).all()
+        z = torch.zeros((M, 64), device=gpu()).bfloat16()
+        z[:, 3], z[:, 4], z[:, 5], z[:, 6] = nan, 100.0, -100.0, -100.0
+        dz = torch.zeros((M, 16), device=gpu()).bfloat16()
+        dz[:, 0] = 1
+        v = torch.ones((16, 64), device=gpu()).bfloat16()
+        v[0, 6] = inf
+        dx = b.bqm_linear_dgrad(dz, v, empty(M, 64), zx=z, act=a, ws=workspace(M, 16, 64))
+        dy = torch.ones((M, 64), device=gpu()).bfloat16()
+        dy[:, 6] = inf
+        for got in (dx, b.bqm_act_grad(dy, z, a, empty(M, 64)), b.bqm_act_grad(dy[:, :7].contiguous(), z[:, :7].contiguous(), a, empty(M, 7))):
+            assert (got[:, 3] == 1).all() if name == "relu" else got[:, 3].isnan().all()
+            assert (got[:, 4] == 1).all() and (got[:, 5].abs() < 1e-30).all()
+            assert name != "relu" or (got[:, 6] == 0).all()
+
+
 def test_gradients_are_the_differences():
     """<dy, (y(p + h d) - y(p - h d)) / 2 h> of the oracle's forward against the GPU's gradients of
     x, w and b in the direction d, through an activation before and one behind the layer."""
