@@ -138,7 +138,9 @@ def check_wgrad(M, N, K, accumulate, with_bias, seed=0):
 # one row and column of tiles and more, contractions of less than a step, one, parts of one
 SHAPES = [(1, 8, 8), (1, 64, 64), (3, 16, 72), (2, 200, 56), (31, 72, 128), (32, 136, 120), (33, 264, 64), (63, 8, 520),
           (64, 128, 136), (65, 64, 192), (100, 56, 40), (127, 520, 200), (129, 264, 264), (200, 1040, 72), (257, 72, 1040),
-          (300, 392, 648), (5, 2056, 1032), (16, 1032, 2056), (48, 528, 3080), (513, 8, 16)]
+          (300, 392, 648), (5, 2056, 1032), (16, 1032, 2056), (48, 528, 3080), (513, 8, 16),
+          # few rows: contractions of several turns of the waves, columns past the last 16
+          (1, 520, 4104), (2, 24, 1160), (4, 72, 2184), (3, 40, 3208), (4, 8, 8200)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -164,9 +166,13 @@ def test_weight_gradient(M, N, K):
     check_wgrad(M, N, K, True, False)
 
 
-# sizes at which each tile, whole rounds of tiles and split remainders occur
+# sizes at which each tile occurs in each direction, with its last tile filled to each quarter,
+# with the contraction in one part and in several, with and without whole rounds of tiles
 LARGE = [(1111, 2848, 2080), (700, 4104, 520), (2050, 1048, 264), (4100, 512, 136), (150, 4096, 2048), (1000, 1000, 4104),
-         (3000, 2056, 1032), (72, 6144, 2048), (8200, 2304, 96)]
+         (3000, 2056, 1032), (72, 6144, 2048), (8200, 2304, 96), (2817, 392, 2968), (8638, 6568, 72), (899, 1360, 4272),
+         (436, 8896, 8304), (4159, 1336, 904), (1353, 4240, 960), (864, 1560, 5408), (258, 5752, 6120), (8778, 1720, 2928),
+         (5051, 856, 1720), (4128, 7800, 1008), (3906, 1064, 8352), (1158, 2360, 6576), (1160, 2144, 7312), (1100, 40008, 72), (2100, 136, 40008),
+         (5000, 70000, 64)]
 
 
 @pytest.mark.parametrize("M,N,K", LARGE)
@@ -200,11 +206,39 @@ def test_large(M, N, K):
     b.bqm_linear_wgrad(dz, x, dw, dbias=db, ws=ws)
     near(dw, D.T @ X, M * F23 * (D.T.abs() @ X.abs()), "dw")
     near(db, D.sum(0), M * F24 * D.abs().sum(0), "db")
-    # the same bits again
-    again, dw2 = empty(M, N), empty(N, K, dtype=torch.float32)
-    b.bqm_linear_fwd(x, w, again, bias=bias, act=b.ACT_RELU, residual=res, ws=ws)
+    b.bqm_linear_wgrad(dz, x, dw, dbias=db, accumulate=True, ws=ws)
+    near(dw, 2 * (D.T @ X), 2.01 * M * F23 * (D.T.abs() @ X.abs()), "dw, added")
+    near(db, 2 * D.sum(0), 2.01 * M * F24 * D.abs().sum(0), "db, added")
+    # the same bits again, without what changes nothing
+    again, dx2, dw2 = empty(M, N), empty(M, K), empty(N, K, dtype=torch.float32)
+    zero = torch.zeros_like(res), torch.zeros_like(bias), torch.zeros_like(x)
+    b.bqm_linear_fwd(x, w, y, bias=zero[1], act=b.ACT_SILU, residual=zero[0], ws=ws)
+    b.bqm_linear_fwd(x, w, again, act=b.ACT_SILU, z=z, ws=ws)
+    assert torch.equal(again, y)
+    for name in ("none", "silu", "gelu_tanh"):
+        act = act_id(name)
+        b.bqm_linear_fwd(x, w, y, bias=bias, act=act, ws=ws)
+        s, slope = {"none": (1.0, 0.0), "silu": (torch.sigmoid(rz), 1.0),
+                    "gelu_tanh": (torch.sigmoid(2 * oracle.C * (rz + 0.044715 * rz ** 3)), 0.0)}[name]
+        # |2 sqrt(2/pi) (v + 0.044715 v^3)| is at most 1.6 |v| + 0.072 |v|^3
+        t = 0.0 if name == "none" else rz.abs() if slope else 1.6 * rz.abs() + 0.072 * rz.abs() ** 3
+        ry = rz * s
+        near(y, ry, F8 * ry.abs() + 1.01 * (1.13 * e + (4 * t + 17) * F23 * ry.abs() + 1e-36), name)
+        b.bqm_linear_dgrad(dz, w, dx, zx=x, act=act, add=zero[2], ws=ws)
+        b.bqm_linear_dgrad(dz, w, dx2, zx=x, act=act, ws=ws)
+        assert torch.equal(dx, dx2)
+        v = X if name != "none" else 0 * X
+        s = torch.sigmoid(v if slope else 2 * oracle.C * (v + 0.044715 * v ** 3))
+        q = v.abs() * s * (1 - s) * (1.0 if slope else 2 * oracle.C * (1 + 3 * 0.044715 * v * v))
+        g = 1.0 if name == "none" else s + v.sign() * q
+        t = v.abs() if slope else 1.6 * v.abs() + 0.072 * v.abs() ** 3
+        off = 0.0 if name == "none" else (4 * t + 16) * F23 * (s + q) + q / (1 - s) * F23 + 1e-36
+        near(dx, d * g, F8 * (d * g).abs() + 1.01 * (1.13 * N * F23 * (D.abs() @ W.abs()) + d.abs() * off + F23 * (d * g).abs()), name)
+    b.bqm_linear_dgrad(dz, w, dx, add=x, ws=ws)
+    near(dx, d + X, F8 * (d + X).abs() + 1.01 * (N * F23 * (D.abs() @ W.abs()) + F23 * (d + X).abs()), "dx, added to")
+    b.bqm_linear_wgrad(dz, x, dw, ws=ws)
     b.bqm_linear_wgrad(dz, x, dw2, ws=ws)
-    assert torch.equal(again, y) and torch.equal(dw2, dw)
+    assert torch.equal(dw2, dw)
 
 
 def test_past_four_gigabytes():
