@@ -10,6 +10,13 @@
 // contraction contiguous (x and w in the forward, dz in the input gradient) or as rows of the
 // contraction (w in the input gradient, dz and x in the weight gradient); the latter is read
 // from LDS transposed.  No transposed copy of a tensor is made.
+//
+// What bounds it.  Large products: the power the matrix unit draws (69% busy at a clock of 2.0
+// GHz); 16384 x 4096 x 6144 takes 555 us forward, 570 for the input's and 590 for the weight's
+// gradient, 1.4 to 1.5 PFLOP/s.  The 16x16x32 instruction draws less than the 32x32x16 of the
+// same rate.  Small ones: a CU's copies, about 100 GB/s each (32 KB of a 128 x 128 tile's step
+// in 0.33 us), and 4 to 7 us of launch, first copies and epilogue: 1111 x 2848 x 2080 21 us,
+// 203 x 768 x 2048 8.7 us.  Few rows: the weights' bytes.
 #include "common.h"
 
 #include <type_traits>
@@ -278,7 +285,9 @@ struct Smem<BM, BN, NSA, NSB, 0> {
   uint8_t b[NSB][BN * 2 * KS];
 };
 
-// row and column tile of tile L: groups of about G row tiles, column by column
+// row and column tile of tile L: groups of about G row tiles, column by column, so that the tiles
+// in flight on an XCD are about as many rows as columns (G = 1, 16384 x 4096 x 6144: forward 571
+// against 555 us, gradients 598 and 611 against 571 and 590)
 template <int G>
 __device__ __forceinline__ int2 tile_at(const LinParams &p, int L) {
   const int n_g = max((p.NI + G / 2) / G, 1), g = (p.NI + n_g - 1) / n_g;
@@ -298,6 +307,11 @@ __device__ __forceinline__ int2 tile_at(const LinParams &p, int L) {
 // the fragment reads of the next slice and of the copies of a later step, held there by
 // scheduling barriers.  The step's one barrier sits inside its last slice, whose fragments are
 // in registers by then; the copies of step ks + NS start behind it, into the stage just read.
+// Stages: as many as LDS holds.  Of the largest tile's three of A and two of B against two of
+// both: 16384 x 4096 x 6144 555 against 619 us.  128 x 128 columns, four against two: 1111 x 2848
+// x 2080 21.0 against 28.4; 64 x 64, four, three, two: 37 x 6144 x 2048 8.9, 11.2, 17.8 us.  Two
+// groups of four waves that share the steps of one 64 x 64 tile gain nothing (8.8 us): the CU's
+// copies are at their rate.
 //
 // Accumulators hold the product transposed (B x A): register v of lane L of a 16 x 16 block is
 // row L % 16 and column 4 (L / 16) + v.
@@ -401,8 +415,9 @@ struct Tile {
   // leave too few registers).  Slice 1 has the step's barrier behind its first row, from where
   // on this step's stages are filled anew: with B for step ks + NSB, then A for ks + NSA, which
   // goes on in slice 0 of the next step.  The copies are kGap MFMAs apart: the four waves' take
-  // 64 cycles on their way, and closer ones hold up the MFMAs; B, with fewer stages, comes first
-  // as it has the least time.
+  // 64 cycles on their way, and closer ones hold up the MFMAs (one MFMA apart, 16384 x 4096 x
+  // 6144: forward 581 against 555 us, gradients 589 and 610 against 571 and 590); B, with fewer
+  // stages, comes first as it has the least time.
   static constexpr int kGap = 5;
   // MFMAs between the barrier and copy j of a step
   template <int VT>
@@ -890,12 +905,14 @@ __global__ void __launch_bounds__(NTHR, OCC) lin_tiles(LinParams p, ColSums cols
     const bool split = L >= full8 && p.S > 1;
     const int k0 = split ? s * p.per : 0, k1 = split ? min(k0 + p.per, p.nk) : p.nk;
     // (in scalar registers: the divisions that they come from are done in vector ones)
-    t.tile(__builtin_amdgcn_readfirstlane(tile), __builtin_amdgcn_readfirstlane(k0), __builtin_amdgcn_readfirstlane(k1), split ? p.part + ((int64_t)(tile - p.full) * p.S + s) * (T::BM * T::BN) : nullptr);
+    float *part = split ? p.part + ((int64_t)(tile - p.full) * p.S + s) * (T::BM * T::BN) : nullptr;
+    t.tile(__builtin_amdgcn_readfirstlane(tile), __builtin_amdgcn_readfirstlane(k0), __builtin_amdgcn_readfirstlane(k1), part);
   }
 }
 #undef LIN_PIN
 
-// the split tiles' parts added in order, then what the others' epilogue does
+// The split tiles' parts added in order, then what the others' epilogue does.  HBM and the
+// last-level cache bound it: 128 tiles of 256 x 256 in two parts, 18 us, 5.6 TB/s.
 template <int BM, int BN, int GM>
 __global__ void __launch_bounds__(256) join_parts(LinParams p) {
   constexpr int U = BM * BN / 8, UR = BN / 8;  // units of 8 columns, per row
@@ -928,6 +945,10 @@ __global__ void __launch_bounds__(256) join_parts(LinParams p) {
 // of 32; rows of x past the last are the last again), with the next group's loads in flight.
 // Weights are the first operand, so lane l ends with columns 4 (l / 16) + 0..3 of row l % 16 of
 // the result.  The waves' sums are added in their order through LDS.
+//
+// 1, 4 and 8 rows, against the 64-row tile, in us, weights from HBM: of 4096 x 6144 12.7, 14.6 and
+// 15.7 (4 TB/s with one row) against 15.1; of 768 x 2048 5.3, 5.4 and 5.9 against 7.4; of 6144 x
+// 2048 9.0, 9.6 and 10.4 against 8.6.
 constexpr int kFewRows = 4;
 constexpr int FW = 8, FU = 4;  // waves; MFMA steps of 32 per group
 
@@ -1009,6 +1030,7 @@ __global__ void __launch_bounds__(256) zero_f32(float *p, int64_t n) {
 // ---------------------------------------------------------------------------
 // the gradient through an activation alone
 // ---------------------------------------------------------------------------
+// 8 elements per lane, once each: HBM bounds it, 16384 x 4096 in 64 us, 6.3 TB/s; 203 x 768 2.9 us.
 __global__ void __launch_bounds__(256) act_grad_rows(const uint16_t *dy, const uint16_t *z, int act, int64_t n, uint16_t *dz) {
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (i + 8 <= n) {
@@ -1040,10 +1062,23 @@ bqm_status check_linear(const char *who, int64_t M, int64_t N, int64_t K) {
   return BQM_OK;
 }
 
-// A tile's size, its workgroups per CU, and what a step of it and the rest of it take (in ns,
-// with every workgroup slot busy)
+// The tile and its split by what they are expected to take: per round of tiles, the steps of 64
+// and the rest (launch, first copies, epilogue), both measured with every CU busy, and for a split
+// the parts written and read and the join's launch.  Both sides, in us (tiles of 256 x 256, 256 x
+// 128, 128 x 128, 64 x 64, each in the split that is best for it):
+//   forward 37 x 6144 x 2048          15.0  13.0  12.3   8.9
+//           300 x 2048 x 2048         26.4  20.0  15.9   9.0
+//           1111 x 2848 x 2080        36.6  28.9  21.0  34.2
+//           2048 x 4096 x 2048        43.6  33.5  38.7  49.1
+//           4096 x 4096 x 4096         103   119   151   241
+//           16384 x 4096 x 6144        567   682   885  1441
+//   input gradient 203 x 2048 x 768   20.5  14.8  12.6   8.8
+//   weight gradient 203 x 2048 x 768  16.4  10.5   8.1   5.9
+//           16384 x 4096 x 6144        607   668   925  2537   (256 x 256 unsplit: 678)
+// Splits pay where a round of tiles is not whole or has many steps: 64 x 1024 x 8192 takes 23.6
+// us in one part, 11.9 in 16.
 struct Shape {
-  int bm, bn, occ;
+  int bm, bn, occ;     // its size, workgroups per CU
   float step, rest;    // us
   float step2, rest2;  // with two workgroups per CU
 };
@@ -1084,7 +1119,9 @@ Plan plan_of(int64_t I, int64_t J, int64_t C) {
   return best;
 }
 
-// row parts of the column sums: of at least 1024 rows, which take no longer than the tiles beside them
+// Row parts of the column sums: of at least 1024 rows, which take no longer than the tiles beside
+// them (in a launch of their own: 203 x 2048 x 768 9.6 against 6.9 us for the weight's and the
+// bias's gradients, 1111 x 2848 x 2080 31 against 27), and at most 2048 workgroups
 int col_parts(int64_t M, int64_t N) {
   const int64_t most = 2048 / cdiv(N, 64), want = cdiv(M, 1024), n = want < most ? want : most;
   return (int)(n < 1 ? 1 : n);

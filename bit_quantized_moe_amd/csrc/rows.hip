@@ -13,7 +13,7 @@
 // time, all loaded before the first is used.  The experts' rows are read, and all results
 // written, past the caches, the tokens' rows are read through them: 16384 x 8 x 6144, dispatch
 // 307 us (379 with everything past them, 366 with nothing), combine 309 (355, 392), gradient
-// 636 (680, 687), which are 5.9, 6.5 and 5.4 TB/s.
+// 640 (680, 687), which are 5.9, 6.5 and 5.3 TB/s.
 #include "common.h"
 
 namespace bqm {
@@ -21,11 +21,17 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// Pairs in flight per lane, G: 8 for up to kFewTokens tokens, where a load's latency counts, 4
-// for more, where the registers of 8 cost workgroups in flight (16384 x 2 x 768: combine 20.3
-// against 18.1 us, gradient 32.6 against 28.2; 16384 x 8 x 6144 the same within 1%).
+// Pairs in flight per lane, G: 8 for up to kFewTokens tokens, where a load's latency counts
+// (gradient of 64 x 8 x 6144 9.1 us, 10.2 with 4), 4 for more, where the registers of 8 cost
+// workgroups in flight (16384 x 2 x 768: combine 20.0 against 18.0 us, gradient 32.6 against 28.1;
+// 16384 x 8 x 256 33.5 against 29.6, but 16384 x 8 x 128 16.1 against 18.7; 16384 x 8 x 6144 the
+// same within 1%).
 constexpr int64_t kFewTokens = 512;
-constexpr int kPacked = 32;    // units per row up to which a wave takes several tokens
+// Units per row up to which a wave takes several tokens (16384 x 8 x 256 and x 64: combine 14.2
+// and 7.5 us, 20.0 and 16.2 with a token per wave; gradient 29.7 and 12.8 against 39.3 and 28.1).
+constexpr int kPacked = 32;
+// Lanes per token: gradient of 64 x 8 x 6144 9.1 us, 11.7 with up to 256; combine of 16384 x 8 x
+// 6144 308 against 324, dispatch 308 against 304.
 constexpr int kMaxThreads = 1024;
 constexpr int64_t kMaxBlocks = 1 << 21;  // of kMaxThreads: a launch takes less than 2^32 threads in x
 
