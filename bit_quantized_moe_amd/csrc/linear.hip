@@ -942,13 +942,18 @@ __global__ void __launch_bounds__(256) join_parts(LinParams p) {
 // A few rows of x: the weights' bytes bound it, each of which is read once.  A workgroup takes
 // 16 rows of w, each of its FW waves every FW-th group of 128 of the contraction, straight from
 // memory into the operands of the 16x16x32 MFMA (lane l: row l % 16, elements 8 (l / 16) + 0..7
-// of 32; rows of x past the last are the last again), with the next group's loads in flight.
+// of 32; the rows of x past the last stay zeros), with the next group's loads in flight.
 // Weights are the first operand, so lane l ends with columns 4 (l / 16) + 0..3 of row l % 16 of
 // the result.  The waves' sums are added in their order through LDS.
 //
-// 1, 4 and 8 rows, against the 64-row tile, in us, weights from HBM: of 4096 x 6144 12.7, 14.6 and
-// 15.7 (4 TB/s with one row) against 15.1; of 768 x 2048 5.3, 5.4 and 5.9 against 7.4; of 6144 x
-// 2048 9.0, 9.6 and 10.4 against 8.6.
+// The weights go through the caches, whose lines are two loads long (past them 8192 x 8192 with one
+// row takes 30.8 us, 27.7 through them); lanes without a row of x load none (28.5 against 27.3 with
+// 4096 x 6144: 12.5 against 12.2).
+//
+// 1, 4 and 8 rows, against the 64-row tile, in us, weights from HBM: of 4096 x 6144 11.7, 12.2 and
+// 15 (4.3 TB/s with one row) against 15.1; of 768 x 2048 4.9, 5.2 and 5.5 against 7.4; of 6144 x
+// 2048 8.2, 8.6 and 9.4 against 8.7; of 8192 x 8192 27, 27 and 33 against 33.  Where few workgroups
+// stream long rows it is behind (1024 x 8192 11.4 and 12.8 against 9.6).
 constexpr int kFewRows = 4;
 constexpr int FW = 8, FU = 4;  // waves; MFMA steps of 32 per group
 
@@ -958,17 +963,18 @@ __global__ void __launch_bounds__(64 * FW) lin_few(LinParams p) {
   const int K = p.C, M = (int)p.I, N = (int)p.J, n0 = blockIdx.x * 16;
   const int e = 8 * (lane >> 4);
   const uint8_t *wr = p.b + (int64_t)min(n0 + (lane & 15), N - 1) * p.ldb;
-  const uint8_t *xr = p.a + (int64_t)min(lane & 15, M - 1) * p.lda;
+  const uint8_t *xr = p.a + (int64_t)(lane & 15) * p.lda;
   f32x4 acc = {};
-  u32x4 wf[2][FU], xf[2][FU];
+  u32x4 wf[2][FU], xf[2][FU] = {};
+  const bool mine = (lane & 15) < M;
   // group i into set b; what lies past the end of the rows is their last 8 elements again,
   // and zeros before it is used
   auto load = [&](int b, int i) {
 #pragma unroll
-    for (int u = 0; u < FU; ++u) {
-      const int k = 2 * min(32 * (FU * i + u) + e, K - 8);
-      wf[b][u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wr + k));
-      xf[b][u] = *reinterpret_cast<const u32x4 *>(xr + k);
+    for (int u = 0; u < FU; ++u) wf[b][u] = *reinterpret_cast<const u32x4 *>(wr + 2 * min(32 * (FU * i + u) + e, K - 8));
+    if (mine) {
+#pragma unroll
+      for (int u = 0; u < FU; ++u) xf[b][u] = *reinterpret_cast<const u32x4 *>(xr + 2 * min(32 * (FU * i + u) + e, K - 8));
     }
   };
   auto use = [&](int b, int i) {
@@ -986,14 +992,20 @@ __global__ void __launch_bounds__(64 * FW) lin_few(LinParams p) {
                                                     acc, 0, 0, 0);
   };
   const int groups = (K + 32 * FU - 1) / (32 * FU);
-  if (w < groups) load(0, w);
-  for (int i = w; i < groups; i += 2 * FW) {
-    if (i + FW < groups) load(1, i + FW);
+  int i = w;
+  if (i < groups) load(0, i);
+  for (; i + 2 * FW < groups; i += 2 * FW) {
+    load(1, i + FW);
     use(0, i);
-    if (i + FW < groups) {
-      if (i + 2 * FW < groups) load(0, i + 2 * FW);
-      use(1, i + FW);
-    }
+    load(0, i + 2 * FW);
+    use(1, i + FW);
+  }
+  if (i + FW < groups) {
+    load(1, i + FW);
+    use(0, i);
+    use(1, i + FW);
+  } else if (i < groups) {
+    use(0, i);
   }
   *reinterpret_cast<f32x4 *>(&sum[w][lane & 15][4 * (lane >> 4)]) = acc;
   __syncthreads();
