@@ -947,14 +947,19 @@ __global__ void __launch_bounds__(256) join_parts(LinParams p) {
 // the result.  The waves' sums are added in their order through LDS.
 //
 // The weights go through the caches, whose lines are two loads long (past them 8192 x 8192 with one
-// row takes 30.8 us, 27.7 through them); lanes without a row of x load none (28.5 against 27.3 with
-// 4096 x 6144: 12.5 against 12.2).
+// row takes 30.8 us, 27.7 through them); lanes without a row of x load none (with all of them 4096 x
+// 6144 takes 12.2 us instead of 11.6: 4.3 TB/s).
 //
-// 1, 4 and 8 rows, against the 64-row tile, in us, weights from HBM: of 4096 x 6144 11.7, 12.2 and
-// 15 (4.3 TB/s with one row) against 15.1; of 768 x 2048 4.9, 5.2 and 5.5 against 7.4; of 6144 x
-// 2048 8.2, 8.6 and 9.4 against 8.7; of 8192 x 8192 27, 27 and 33 against 33.  Where few workgroups
-// stream long rows it is behind (1024 x 8192 11.4 and 12.8 against 9.6).
-constexpr int kFewRows = 4;
+// 1, 4 and 8 rows, against the 64-row tile, in us, weights from HBM: of 4096 x 6144 11.6, 12.6 and
+// 13.9 against 15.1; of 8192 x 8192 27.6, 27.8 and 29.5 against 33.4; of 6144 x 2048 8.0, 8.5 and
+// 9.3 against 8.7; of 768 x 2048 4.8, 5.1 and 5.5 against 7.4; of 256 x 1024 3.4, 3.5 and 3.7
+// against 5.3; with 16 rows of these 15.9, 35.3, 10.3, 6.3 and 4.0.  A workgroup's stream takes 1.0
+// us per 1024 of the contraction, so that where few of them have long rows the tiles, which split
+// the contraction over idle CUs, are ahead: 1, 4 and 8 rows of 1024 x 8192 11.3, 12.7 and 14.2
+// against 9.6, of 2048 x 8192 12.1, 13.4 and 14.9 against 11.7; of 1024 x 4096 7.1, 7.8 and 8.5
+// against 8.5.
+constexpr int kFewRows = 8;
+bool few_rows(int64_t M, int64_t N, int64_t K) { return M <= kFewRows && (K <= 4096 || 2 * N >= K); }
 constexpr int FW = 8, FU = 4;  // waves; MFMA steps of 32 per group
 
 __global__ void __launch_bounds__(64 * FW) lin_few(LinParams p) {
@@ -1199,7 +1204,7 @@ using namespace bqm;
 
 extern "C" size_t bqm_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (check_linear("bqm_linear_workspace_size", M, N, K) != BQM_OK || M == 0) return 0;
-  int64_t most = M <= kFewRows ? 0 : plan_of(M, N, K).part;
+  int64_t most = few_rows(M, N, K) ? 0 : plan_of(M, N, K).part;
   const int64_t d = plan_of(M, K, N).part, w = wgrad_floats(M, N, K);
   most = d > most ? d : most;
   return ws_size(w > most ? w : most);
@@ -1215,7 +1220,7 @@ extern "C" bqm_status bqm_linear_fwd(const uint16_t *x, const uint16_t *w, const
   BQM_REQUIRE(x && w && y, BQM_ERR_INVALID_ARG, "%s: x, w or y is NULL", who);
   BQM_REQUIRE(aligned16(x) && aligned16(w) && aligned16(bias) && aligned16(residual) && aligned16(y) && aligned16(z),
               BQM_ERR_ALIGN, "%s: pointer not 16-byte aligned", who);
-  const bool few = M <= kFewRows;
+  const bool few = few_rows(M, N, K);
   const Plan plan = few ? Plan{} : plan_of(M, N, K);
   st = check_ws(who, ws, ws_bytes, (size_t)plan.part * 4);
   if (st != BQM_OK) return st;

@@ -140,7 +140,8 @@ SHAPES = [(1, 8, 8), (1, 64, 64), (3, 16, 72), (2, 200, 56), (31, 72, 128), (32,
           (64, 128, 136), (65, 64, 192), (100, 56, 40), (127, 520, 200), (129, 264, 264), (200, 1040, 72), (257, 72, 1040),
           (300, 392, 648), (5, 2056, 1032), (16, 1032, 2056), (48, 528, 3080), (513, 8, 16),
           # few rows: contractions of several turns of the waves, columns past the last 16
-          (1, 520, 4104), (2, 24, 1160), (4, 72, 2184), (3, 40, 3208), (4, 8, 8200)]
+          (1, 520, 4104), (2, 24, 1160), (4, 72, 2184), (3, 40, 3208), (4, 8, 8200), (8, 24, 4096), (7, 2056, 4104), (6, 40, 72),
+          (8, 2048, 4104)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
