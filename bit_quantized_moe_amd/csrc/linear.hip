@@ -1092,15 +1092,18 @@ bqm_status check_linear(const char *who, int64_t M, int64_t N, int64_t K) {
 //   input gradient 203 x 2048 x 768   20.5  14.8  12.6   8.8
 //   weight gradient 203 x 2048 x 768  16.4  10.5   8.1   5.9
 //           16384 x 4096 x 6144        607   668   925  2537   (256 x 256 unsplit: 678)
-// Splits pay where a round of tiles is not whole or has many steps: 64 x 1024 x 8192 takes 23.6
+// Rows that start off 64 bytes cost a large tile's copies least: forward 799 x 3032 x 6192, 256 x
+// 256 tiles in five parts 56 us, 256 x 128 in two 69, 128 x 128 68; 600 x 4096 x 4096 41 (four
+// parts), 36 (two), 35.6.  Splits pay where a round of tiles is not whole or has many steps: 64 x 1024 x 8192 takes 23.6
 // us in one part, 11.9 in 16.
 struct Shape {
   int bm, bn, occ;     // its size, workgroups per CU
   float step, rest;    // us
   float step2, rest2;  // with two workgroups per CU
+  float odd;           // a step's factor where an operand's rows start off 64 bytes
 };
-constexpr Shape kShapes[4] = {{256, 256, 1, 1.0f, 12.4f, 0, 0}, {256, 128, 1, .53f, 8.6f, 0, 0},
-                              {128, 128, 1, .42f, 7.0f, 0, 0}, {64, 64, 2, .19f, 5.7f, .60f, 4.5f}};
+constexpr Shape kShapes[4] = {{256, 256, 1, 1.0f, 12.4f, 0, 0, 1.15f}, {256, 128, 1, .62f, 8.6f, 0, 0, 1.35f},
+                              {128, 128, 1, .42f, 7.0f, 0, 0, 1.3f}, {64, 64, 2, .19f, 5.7f, .60f, 4.5f, 1.3f}};
 constexpr float kJoin = 4.6f, kJoinRate = 7.5e6f;  // us of a join's launch; its bytes per us
 constexpr int kSlow = 2;  // the shape for contractions of less than a step
 
@@ -1109,7 +1112,8 @@ struct Plan {
   int64_t part;  // floats of the workspace
 };
 
-Plan plan_of(int64_t I, int64_t J, int64_t C) {
+// odd: an operand's rows are no multiple of 64 bytes
+Plan plan_of(int64_t I, int64_t J, int64_t C, bool odd) {
   Plan best = {};
   float least = 0.0f;
   for (int h = 0; h < 4; ++h) {
@@ -1123,7 +1127,7 @@ Plan plan_of(int64_t I, int64_t J, int64_t C) {
       const int per = (int)cdiv(nk, S);
       if (S > 1 && (rem == 0 || rem * S > slots || per < 2)) break;
       if (S > 1 && (int64_t)per * (S - 1) >= nk) continue;  // a part without steps
-      const float step = two ? s.step2 : s.step, rest = two ? s.rest2 : s.rest;
+      const float step = two ? s.step2 : odd ? s.step * s.odd : s.step, rest = two ? s.rest2 : s.rest;
       float t = full / slots * (nk * step + rest);
       if (rem) t += per * step + rest;
       if (S > 1) t += kJoin + 8.0f * rem * S * s.bm * s.bn / kJoinRate;  // written and read
@@ -1136,6 +1140,10 @@ Plan plan_of(int64_t I, int64_t J, int64_t C) {
   return best;
 }
 
+Plan plan_fwd(int64_t M, int64_t N, int64_t K) { return plan_of(M, N, K, K % 32); }
+Plan plan_dgrad(int64_t M, int64_t N, int64_t K) { return plan_of(M, K, N, N % 32 || K % 32); }
+Plan plan_wgrad(int64_t M, int64_t N, int64_t K) { return plan_of(N, K, M, N % 32 || K % 32); }
+
 // Row parts of the column sums: of at least 1024 rows, which take no longer than the tiles beside
 // them (in a launch of their own: 203 x 2048 x 768 9.6 against 6.9 us for the weight's and the
 // bias's gradients, 1111 x 2848 x 2080 31 against 27), and at most 2048 workgroups
@@ -1147,7 +1155,7 @@ int col_parts(int64_t M, int64_t N) {
 // floats of the workspace that a direction takes
 int64_t wgrad_floats(int64_t M, int64_t N, int64_t K) {
   const int parts = col_parts(M, N);
-  const int64_t a = plan_of(N, K, M).part, b = parts > 1 ? parts * N : 0;
+  const int64_t a = plan_wgrad(M, N, K).part, b = parts > 1 ? parts * N : 0;
   return a + b;
 }
 size_t ws_size(int64_t floats) { return align256((size_t)floats * 4); }
@@ -1204,8 +1212,8 @@ using namespace bqm;
 
 extern "C" size_t bqm_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (check_linear("bqm_linear_workspace_size", M, N, K) != BQM_OK || M == 0) return 0;
-  int64_t most = few_rows(M, N, K) ? 0 : plan_of(M, N, K).part;
-  const int64_t d = plan_of(M, K, N).part, w = wgrad_floats(M, N, K);
+  int64_t most = few_rows(M, N, K) ? 0 : plan_fwd(M, N, K).part;
+  const int64_t d = plan_dgrad(M, N, K).part, w = wgrad_floats(M, N, K);
   most = d > most ? d : most;
   return ws_size(w > most ? w : most);
 }
@@ -1221,7 +1229,7 @@ extern "C" bqm_status bqm_linear_fwd(const uint16_t *x, const uint16_t *w, const
   BQM_REQUIRE(aligned16(x) && aligned16(w) && aligned16(bias) && aligned16(residual) && aligned16(y) && aligned16(z),
               BQM_ERR_ALIGN, "%s: pointer not 16-byte aligned", who);
   const bool few = few_rows(M, N, K);
-  const Plan plan = few ? Plan{} : plan_of(M, N, K);
+  const Plan plan = few ? Plan{} : plan_fwd(M, N, K);
   st = check_ws(who, ws, ws_bytes, (size_t)plan.part * 4);
   if (st != BQM_OK) return st;
   LinParams p = {};
@@ -1248,7 +1256,7 @@ extern "C" bqm_status bqm_linear_dgrad(const uint16_t *dz, const uint16_t *w, co
   BQM_REQUIRE(zx || act == BQM_ACT_NONE, BQM_ERR_INVALID_ARG, "%s: an activation needs zx", who);
   BQM_REQUIRE(aligned16(dz) && aligned16(w) && aligned16(zx) && aligned16(add) && aligned16(dx), BQM_ERR_ALIGN,
               "%s: pointer not 16-byte aligned", who);
-  const Plan plan = plan_of(M, K, N);
+  const Plan plan = plan_dgrad(M, N, K);
   st = check_ws(who, ws, ws_bytes, (size_t)plan.part * 4);
   if (st != BQM_OK) return st;
   LinParams p = {};
@@ -1276,7 +1284,7 @@ extern "C" bqm_status bqm_linear_wgrad(const uint16_t *dz, const uint16_t *x, in
     if (dbias) zero_f32<<<(unsigned)cdiv(N, 256), 256, 0, s>>>(dbias, N);
     return launch_status(who);
   }
-  const Plan plan = plan_of(N, K, M);
+  const Plan plan = plan_wgrad(M, N, K);
   const int parts = dbias ? col_parts(M, N) : 1;
   st = check_ws(who, ws, ws_bytes, (size_t)(plan.part + (parts > 1 ? parts * N : 0)) * 4);
   if (st != BQM_OK) return st;

@@ -173,7 +173,7 @@ LARGE = [(1111, 2848, 2080), (700, 4104, 520), (2050, 1048, 264), (4100, 512, 13
          (3000, 2056, 1032), (72, 6144, 2048), (8200, 2304, 96), (2817, 392, 2968), (8638, 6568, 72), (899, 1360, 4272),
          (436, 8896, 8304), (4159, 1336, 904), (1353, 4240, 960), (864, 1560, 5408), (258, 5752, 6120), (8778, 1720, 2928),
          (5051, 856, 1720), (4128, 7800, 1008), (3906, 1064, 8352), (1158, 2360, 6576), (1160, 2144, 7312), (1100, 40008, 72), (2100, 136, 40008),
-         (5000, 70000, 64)]
+         (5000, 70000, 64), (6515, 136, 6512), (8792, 3216, 136), (5927, 5312, 136)]
 
 
 @pytest.mark.parametrize("M,N,K", LARGE)
