@@ -525,6 +525,7 @@ def bqm_combine_grad(dout, inv, y=None, topk_w=None, dy=None, dtopk_w=None, n_ro
 
 
 def bqm_linear_workspace_size(M, N, K) -> int:
+    """Bytes of ws for the three products with weights [N, K] and up to M rows."""
     return load().bqm_linear_workspace_size(M, N, K)
 
 

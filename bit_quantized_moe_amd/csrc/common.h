@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "bqm.h"
+#include "sizes.h"
 
 namespace bqm {
 
@@ -16,8 +17,6 @@ bqm_status launch_status(const char *what);
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline hipStream_t as_stream(void *s) { return reinterpret_cast<hipStream_t>(s); }
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
 // ---------------------------------------------------------------------------
 // device-side number-format helpers (bit-exact; compiled with -ffp-contract=off)

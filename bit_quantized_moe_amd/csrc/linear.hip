@@ -18,6 +18,7 @@
 // in 0.33 us), and 4 to 7 us of launch, first copies and epilogue: 1111 x 2848 x 2080 21 us,
 // 203 x 768 x 2048 8.7 us.  Few rows: the weights' bytes.
 #include "common.h"
+#include "linear_plan.h"
 
 #include <type_traits>
 
@@ -35,8 +36,6 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
 
 constexpr int NTHR = 256;  // four waves, one per SIMD
-constexpr int kCUs = 256;
-constexpr int KS = 64;  // contraction per step: 128 bytes of a row
 
 enum Mode { FWD, DGRAD, WGRAD };
 
@@ -958,8 +957,6 @@ __global__ void __launch_bounds__(256) join_parts(LinParams p) {
 // the contraction over idle CUs, are ahead: 1, 4 and 8 rows of 1024 x 8192 11.3, 12.7 and 14.2
 // against 9.6, of 2048 x 8192 12.1, 13.4 and 14.9 against 11.7; of 1024 x 4096 7.1, 7.8 and 8.5
 // against 8.5.
-constexpr int kFewRows = 8;
-bool few_rows(int64_t M, int64_t N, int64_t K) { return M <= kFewRows && (K <= 4096 || 2 * N >= K); }
 constexpr int FW = 8, FU = 4;  // waves; MFMA steps of 32 per group
 
 __global__ void __launch_bounds__(64 * FW) lin_few(LinParams p) {
@@ -1079,87 +1076,6 @@ bqm_status check_linear(const char *who, int64_t M, int64_t N, int64_t K) {
   return BQM_OK;
 }
 
-// The tile and its split by what they are expected to take: per round of tiles, the steps of 64
-// and the rest (launch, first copies, epilogue), both measured with every CU busy, and for a split
-// the parts written and read and the join's launch.  Both sides, in us (tiles of 256 x 256, 256 x
-// 128, 128 x 128, 64 x 64, each in the split that is best for it):
-//   forward 37 x 6144 x 2048          15.0  13.0  12.3   8.9
-//           300 x 2048 x 2048         26.4  20.0  15.9   9.0
-//           1111 x 2848 x 2080        36.6  28.9  21.0  34.2
-//           2048 x 4096 x 2048        43.6  33.5  38.7  49.1
-//           4096 x 4096 x 4096         103   119   151   241
-//           16384 x 4096 x 6144        567   682   885  1441
-//   input gradient 203 x 2048 x 768   20.5  14.8  12.6   8.8
-//   weight gradient 203 x 2048 x 768  16.4  10.5   8.1   5.9
-//           16384 x 4096 x 6144        607   668   925  2537   (256 x 256 unsplit: 678)
-// Rows that start off 64 bytes cost a large tile's copies least: forward 799 x 3032 x 6192, 256 x
-// 256 tiles in five parts 56 us, 256 x 128 in two 69, 128 x 128 68; 600 x 4096 x 4096 41 (four
-// parts), 36 (two), 35.6.  Splits pay where a round of tiles is not whole or has many steps: 64 x 1024 x 8192 takes 23.6
-// us in one part, 11.9 in 16.
-struct Shape {
-  int bm, bn, occ;     // its size, workgroups per CU
-  float step, rest;    // us
-  float step2, rest2;  // with two workgroups per CU
-  float odd;           // a step's factor where an operand's rows start off 64 bytes
-};
-constexpr Shape kShapes[4] = {{256, 256, 1, 1.0f, 12.4f, 0, 0, 1.15f}, {256, 128, 1, .62f, 8.6f, 0, 0, 1.35f},
-                              {128, 128, 1, .42f, 7.0f, 0, 0, 1.3f}, {64, 64, 2, .19f, 5.7f, .60f, 4.5f, 1.3f}};
-constexpr float kJoin = 4.6f, kJoinRate = 7.5e6f;  // us of a join's launch; its bytes per us
-constexpr int kSlow = 2;  // the shape for contractions of less than a step
-
-struct Plan {
-  int shape, NI, NJ, full, rem, S, per, nk;
-  int64_t part;  // floats of the workspace
-};
-
-// odd: an operand's rows are no multiple of 64 bytes
-Plan plan_of(int64_t I, int64_t J, int64_t C, bool odd) {
-  Plan best = {};
-  float least = 0.0f;
-  for (int h = 0; h < 4; ++h) {
-    const Shape &s = kShapes[h];
-    if (C < 64 && h != kSlow) continue;
-    const int64_t tiles = cdiv(I, s.bm) * cdiv(J, s.bn);
-    const int nk = (int)cdiv(C, KS);
-    for (int S = 1; S <= 32; ++S) {
-      const bool two = s.occ == 2 && tiles * S > kCUs;
-      const int64_t slots = two ? 2 * kCUs : kCUs, full = tiles / slots * slots, rem = tiles - full;
-      const int per = (int)cdiv(nk, S);
-      if (S > 1 && (rem == 0 || rem * S > slots || per < 2)) break;
-      if (S > 1 && (int64_t)per * (S - 1) >= nk) continue;  // a part without steps
-      const float step = two ? s.step2 : odd ? s.step * s.odd : s.step, rest = two ? s.rest2 : s.rest;
-      float t = full / slots * (nk * step + rest);
-      if (rem) t += per * step + rest;
-      if (S > 1) t += kJoin + 8.0f * rem * S * s.bm * s.bn / kJoinRate;  // written and read
-      if (least == 0.0f || t < least) {
-        least = t;
-        best = {h, (int)cdiv(I, s.bm), (int)cdiv(J, s.bn), (int)full, (int)rem, S, per, nk, S > 1 ? rem * S * s.bm * s.bn : 0};
-      }
-    }
-  }
-  return best;
-}
-
-Plan plan_fwd(int64_t M, int64_t N, int64_t K) { return plan_of(M, N, K, K % 32); }
-Plan plan_dgrad(int64_t M, int64_t N, int64_t K) { return plan_of(M, K, N, N % 32 || K % 32); }
-Plan plan_wgrad(int64_t M, int64_t N, int64_t K) { return plan_of(N, K, M, N % 32 || K % 32); }
-
-// Row parts of the column sums: of at least 1024 rows, which take no longer than the tiles beside
-// them (in a launch of their own: 203 x 2048 x 768 9.6 against 6.9 us for the weight's and the
-// bias's gradients, 1111 x 2848 x 2080 31 against 27), and at most 2048 workgroups
-int col_parts(int64_t M, int64_t N) {
-  const int64_t most = 2048 / cdiv(N, 64), want = cdiv(M, 1024), n = want < most ? want : most;
-  return (int)(n < 1 ? 1 : n);
-}
-
-// floats of the workspace that a direction takes
-int64_t wgrad_floats(int64_t M, int64_t N, int64_t K) {
-  const int parts = col_parts(M, N);
-  const int64_t a = plan_wgrad(M, N, K).part, b = parts > 1 ? parts * N : 0;
-  return a + b;
-}
-size_t ws_size(int64_t floats) { return align256((size_t)floats * 4); }
-
 template <bool AT, bool BT>
 bqm_status launch_tiles(LinParams p, const Plan &plan, hipStream_t s, const char *what, const ColSums &cols = {}) {
   p.NI = plan.NI, p.NJ = plan.NJ, p.full = plan.full, p.rem = plan.rem, p.S = plan.S, p.per = plan.per, p.nk = plan.nk;
@@ -1212,10 +1128,7 @@ using namespace bqm;
 
 extern "C" size_t bqm_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (check_linear("bqm_linear_workspace_size", M, N, K) != BQM_OK || M == 0) return 0;
-  int64_t most = few_rows(M, N, K) ? 0 : plan_fwd(M, N, K).part;
-  const int64_t d = plan_dgrad(M, N, K).part, w = wgrad_floats(M, N, K);
-  most = d > most ? d : most;
-  return ws_size(w > most ? w : most);
+  return align256((size_t)workspace_floats(M, N, K) * 4);
 }
 
 extern "C" bqm_status bqm_linear_fwd(const uint16_t *x, const uint16_t *w, const uint16_t *bias, int32_t act,
@@ -1286,7 +1199,7 @@ extern "C" bqm_status bqm_linear_wgrad(const uint16_t *dz, const uint16_t *x, in
   }
   const Plan plan = plan_wgrad(M, N, K);
   const int parts = dbias ? col_parts(M, N) : 1;
-  st = check_ws(who, ws, ws_bytes, (size_t)(plan.part + (parts > 1 ? parts * N : 0)) * 4);
+  st = check_ws(who, ws, ws_bytes, (size_t)(plan.part + (dbias ? col_floats(M, N) : 0)) * 4);
   if (st != BQM_OK) return st;
   LinParams p = {};
   p.mode = WGRAD, p.accumulate = accumulate != 0;

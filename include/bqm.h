@@ -338,9 +338,11 @@ bqm_status bqm_combine_grad(const uint16_t *dout, const uint16_t *y, const int32
  * A NaN in v is a NaN in act(v) and in the gradient through it (ReLU: the gradient passes).
  *
  * ws: bqm_linear_workspace_size() bytes of device scratch, for partial sums where the
- * contraction is split over workgroups (0 bytes, and NULL, where no direction needs any); the
- * size covers all three directions.  Calls that share one ws must not overlap.  Results are
- * the same bits in every call with the same sizes. */
+ * contraction is split over workgroups (0 bytes, and NULL, where no direction needs any).  The
+ * size covers all three directions and every smaller M with the same N and K, so that one made
+ * for the largest batch serves all of them; it is at most 65 MiB, and what a call needs may be
+ * less.  Calls that share one ws must not overlap.  Results are the same bits in every call with
+ * the same sizes, whatever the size of ws. */
 typedef enum { BQM_ACT_NONE = 0, BQM_ACT_RELU = 1, BQM_ACT_SILU = 2, BQM_ACT_GELU_TANH = 3 } bqm_act;
 
 size_t bqm_linear_workspace_size(int64_t M, int64_t N, int64_t K);

@@ -482,3 +482,31 @@ def test_binding_checks_every_tensor():
                 with pytest.raises((b.BQMError, ValueError)):
                     f(*args[:i], other, *args[i + 1:])
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("most,N,K", [(1024, 4096, 6144), (600, 2056, 3080), (16384, 264, 264)])
+def test_one_workspace_for_every_batch(most, N, K):
+    """A workspace made for the largest batch serves the smaller ones, with the same bits as any other."""
+    import torch
+    log(f"one workspace {most} {N} {K}")
+    b = _bqm()
+    g = torch.Generator(device=gpu()).manual_seed(most)
+    rnd = lambda *s: torch.randn(s, generator=g, device=gpu()).to(torch.bfloat16)  # noqa: E731
+    x, w, dz, ws = rnd(most, K), rnd(N, K), rnd(most, N), workspace(most, N, K)
+    larger = torch.full((ws.numel() + 4096,), 0xFF, dtype=torch.uint8, device=gpu())
+    X, W, D = x.double(), w.double(), dz.double()
+
+    def near(got, ref, err):
+        assert ((got.double() - ref).abs() <= err).all()
+
+    for M in [m for m in (1, 8, 9, 37, 100, 300, 500, 512, 513, 600, 1000, 1024, 8192, 16384) if m <= most]:
+        xs, ds = x[:M], dz[:M]
+        out = [[b.bqm_linear_fwd(xs, w, empty(M, N), ws=s), b.bqm_linear_dgrad(ds, w, empty(M, K), ws=s),
+                b.bqm_linear_wgrad(ds, xs, empty(N, K, dtype=torch.float32), ws=s)] for s in (ws, larger)]
+        assert all(torch.equal(p, q) for p, q in zip(*out)), M
+        y, dx, dw = out[0]
+        ref = X[:M] @ W.T
+        near(y, ref, F8 * ref.abs() + 1.01 * K * F23 * (X[:M].abs() @ W.abs().T))
+        ref = D[:M] @ W
+        near(dx, ref, F8 * ref.abs() + 1.01 * N * F23 * (D[:M].abs() @ W.abs()))
+        near(dw, D[:M].T @ X[:M], M * F23 * (D[:M].abs().T @ X[:M].abs()))
