@@ -510,3 +510,69 @@ def test_one_workspace_for_every_batch(most, N, K):
         ref = D[:M] @ W
         near(dx, ref, F8 * ref.abs() + 1.01 * N * F23 * (D[:M].abs() @ W.abs()))
         near(dw, D[:M].T @ X[:M], M * F23 * (D[:M].abs().T @ X[:M].abs()))
+
+
+@pytest.mark.parametrize("name", ACTS[1:])
+def test_gradients_along_themselves(name):
+    """Differences of the oracle's forward along the signs of each gradient, where all terms add up,
+    so that what is allowed (each element's rounding, as in the tests above) is small beside them.
+    The two steps apart, each on the bf16 values it is given: z to act(z), and (zx, w, b) to
+    act(zx) w^T + b.  Third derivatives of the activations stay below 4: central differences with
+    h = 1e-4 are off by less than 1e-8 of the sum of the weights; float64 sums by less than 1e-7."""
+    import torch
+    log(f"gradients along themselves {name}")
+    b = _bqm()
+    M, N, K, h = 9, 40, 72, 1e-4
+    rng = np.random.default_rng(17)
+    z, zx, dy, dz, x = (bf16(rng.standard_normal(s)) for s in ((M, N), (M, K), (M, N), (M, N), (M, K)))
+    w, bias = bf16(rng.standard_normal((N, K)) / 8), bf16(rng.standard_normal(N))
+    assert min(np.abs(z).min(), np.abs(zx).min()) > 2 * h      # off ReLU's corner
+    a = act_id(name)
+    g_z = b.bqm_act_grad(dev_bf16(dy), dev_bf16(z), a, empty(M, N))
+    g_zx = b.bqm_linear_dgrad(dev_bf16(dz), dev_bf16(w), empty(M, K), zx=dev_bf16(zx), act=a, ws=workspace(M, N, K))
+    g_w, g_b = empty(N, K, dtype=torch.float32), empty(N, dtype=torch.float32)
+    b.bqm_linear_wgrad(dev_bf16(dz), dev_bf16(x), g_w, dbias=g_b, ws=workspace(M, N, K))
+    D, W = np.abs(dz), np.abs(w)
+    ref_z = dy * oracle.act_grad(z, name)
+    ref_zx, d, mag = oracle.dgrad(dz, w, zx, name, None)
+    rw, mw, rb, mb = oracle.wgrad(dz, x)
+    layer = lambda zx_, w_, b_: (dz * (oracle.act(zx_, name) @ w_.T + b_)).sum()  # noqa: E731
+    plain = lambda w_, b_: (dz * (x @ w_.T + b_)).sum()  # noqa: E731
+    for what, got, ref, f, err, weights in [
+        ("z", g_z, ref_z, lambda s: (dy * oracle.act(z + s, name)).sum(),
+         rounded(ref_z, np.abs(dy) * eval_err(z, name, True) + F23 * np.abs(ref_z)), np.abs(dy)),
+        ("zx", g_zx, ref_zx, lambda s: layer(zx + s, w, bias),
+         rounded(ref_zx, 1.13 * N * F23 * mag + np.abs(d) * eval_err(zx, name, True) + 2 * F23 * np.abs(ref_zx)), D @ W),
+        ("w", g_w, rw, lambda s: plain(w + s, bias), M * F23 * mw, mw),
+        ("b", g_b, rb, lambda s: plain(w, bias + s), M * F24 * mb, mb),
+    ]:
+        step = np.sign(ref)
+        num, ana = (f(h * step) - f(-h * step)) / (2 * h), (host(got) * step).sum()
+        allowed = err.sum() + 2e-7 * weights.sum()
+        assert allowed < 0.01 * np.abs(ref).sum() and abs(num - np.abs(ref).sum()) < 2e-7 * weights.sum(), what
+        assert abs(num - ana) <= allowed, (what, num, ana, allowed)
+
+
+def test_past_four_gigabytes_exactly():
+    """Whole numbers of up to 3 in 400003 x 6144: every product and sum is exact (below 2^24), so
+    each row of the result and each row's part of the gradients counts."""
+    import torch
+    log("past 4 GiB, whole numbers")
+    b = _bqm()
+    M, N, K = 400003, 64, 6144
+    g = torch.Generator(device=gpu()).manual_seed(4)
+    some = lambda *s: torch.randint(-3, 4, s, generator=g, device=gpu(), dtype=torch.int8).bfloat16()  # noqa: E731
+    x, w, dz = some(M, K), some(N, K), some(M, N)
+    ws = workspace(M, N, K)
+    y = b.bqm_linear_fwd(x, w, empty(M, N), ws=ws)
+    dx = b.bqm_linear_dgrad(dz, w, empty(M, K), ws=ws)
+    dw, db = empty(N, K, dtype=torch.float32), empty(N, dtype=torch.float32)
+    b.bqm_linear_wgrad(dz, x, dw, dbias=db, ws=ws)
+    W, ref = w.double(), torch.zeros((N, K), dtype=torch.float64, device=gpu())
+    for i in range(0, M, 50000):
+        X, D = x[i:i + 50000].double(), dz[i:i + 50000].double()
+        assert torch.equal(y[i:i + 50000], (X @ W.T).bfloat16()), i
+        assert torch.equal(dx[i:i + 50000], (D @ W).bfloat16()), i
+        ref += D.T @ X
+    assert torch.equal(dw.double(), ref)
+    assert torch.equal(db.double(), dz.double().sum(0))
