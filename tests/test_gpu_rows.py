@@ -257,3 +257,20 @@ def test_binding_checks_every_tensor():
                 with pytest.raises((b.BQMError, ValueError)):
                     f(*args[:i], other, *args[i + 1:])
     torch.cuda.synchronize()
+
+
+# more than 512 tokens, where a lane has four pairs in flight: up to four, more, and several turns of
+# them; several tokens per wave, one, and rows of single elements
+MANY = [(513, 1, 264), (700, 8, 264), (600, 6, 64), (520, 9, 7), (515, 5, 2080), (530, 17, 24), (1025, 4, 601), (514, 12, 33),
+        (777, 7, 256), (513, 3, 8200)]
+
+
+@pytest.mark.parametrize("kind", ["all", "dropped", "none"])
+@pytest.mark.parametrize("T,k,H", MANY)
+def test_many_tokens_against_oracle(T, k, H, kind):
+    test_against_oracle(T, k, H, kind)
+
+
+@pytest.mark.parametrize("T,k,H", [(600, 8, 264), (513, 6, 40), (555, 9, 601)])
+def test_many_tokens_in_place(T, k, H):
+    test_in_place(T, k, H)
