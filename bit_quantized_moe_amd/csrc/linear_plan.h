@@ -32,12 +32,17 @@ inline bool few_rows(int64_t M, int64_t N, int64_t K) { return M <= kFewRows && 
 // Rows that start off 64 bytes cost a large tile's copies least: forward 799 x 3032 x 6192, 256 x
 // 256 tiles in five parts 56 us, 256 x 128 in two 69, 128 x 128 68; 600 x 4096 x 4096 41 (four
 // parts), 36 (two), 35.6.  Splits pay where a round of tiles is not whole or has many steps: 64 x 1024 x 8192 takes 23.6
-// us in one part, 11.9 in 16.
+// us in one part, 11.9 in 16.  Tiles that leave CUs idle are split into one part per CU at most, as
+// two workgroups on a CU share its copies and there are more parts to join: input gradient 72 x 3064 x
+// 472 in 16 parts 8.7 us, in 24 10.7; 60 drawn sizes take 0.75 to 1.02 times as long as with two, 0.86
+// in the mean.  step2 is more than two unsplit workgroups take (.31 to .40, and .51 to .55 with rows off
+// 64 bytes), so it has no factor: with one, 19 drawn sizes get 128 x 128 tiles and take 0.94 to 1.26
+// times as long (input gradient 345 x 776 x 3064 11.3 us, 64 x 64 tiles 9.4).
 struct Shape {
   int bm, bn, occ;     // its size, workgroups per CU
   float step, rest;    // us
   float step2, rest2;  // with two workgroups per CU
-  float odd;           // a step's factor where an operand's rows start off 64 bytes
+  float odd;           // factor of step where an operand's rows start off 64 bytes
 };
 constexpr Shape kShapes[4] = {{256, 256, 1, 1.0f, 12.4f, 0, 0, 1.15f}, {256, 128, 1, .62f, 8.6f, 0, 0, 1.35f},
                               {128, 128, 1, .42f, 7.0f, 0, 0, 1.3f}, {64, 64, 2, .19f, 5.7f, .60f, 4.5f, 1.3f}};
@@ -61,9 +66,9 @@ inline Plan plan_of(int64_t I, int64_t J, int64_t C, bool odd) {
     if (C < 64 && h != kSlow) continue;
     const int64_t tiles = cdiv(I, s.bm) * cdiv(J, s.bn);
     const int nk = (int)cdiv(C, KS);
+    const bool two = s.occ == 2 && tiles > kCUs;
+    const int64_t slots = two ? 2 * kCUs : kCUs, full = tiles / slots * slots, rem = tiles - full;
     for (int S = 1; S <= kMostParts; ++S) {
-      const bool two = s.occ == 2 && tiles * S > kCUs;
-      const int64_t slots = two ? 2 * kCUs : kCUs, full = tiles / slots * slots, rem = tiles - full;
       const int per = (int)cdiv(nk, S);
       if (S > 1 && (rem == 0 || rem * S > slots || per < 2)) break;
       if (S > 1 && (int64_t)per * (S - 1) >= nk) continue;  // a part without steps

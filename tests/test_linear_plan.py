@@ -21,6 +21,12 @@ int64_t need(int64_t M, int64_t N, int64_t K, int dir) {
   if (dir == 0) return few_rows(M, N, K) ? 0 : plan_fwd(M, N, K).part;
   return dir == 1 ? plan_dgrad(M, N, K).part : plan_wgrad(M, N, K).part + col_floats(M, N);
 }
+// tile's rows and columns, whole tiles, those left over, their parts, steps per part, steps
+void plan_at(int64_t M, int64_t N, int64_t K, int dir, int64_t *o) {
+  const Plan p = dir == 0 ? plan_fwd(M, N, K) : dir == 1 ? plan_dgrad(M, N, K) : plan_wgrad(M, N, K);
+  const int64_t v[7] = {kShapes[p.shape].bm, kShapes[p.shape].bn, p.full, p.rem, p.S, p.per, p.nk};
+  for (int i = 0; i < 7; ++i) o[i] = v[i];
+}
 int64_t enough(int64_t M, int64_t N, int64_t K) { return workspace_floats(M, N, K); }
 // the first row count up to M that needs more than has been promised, or 0; every one of them
 // in steps, and those on either side of a row of tiles
@@ -55,6 +61,8 @@ def plan(tmp_path_factory):
     for f, n in (("need", 3), ("enough", 3), ("short_of", 4)):
         getattr(lib, f).restype = C.c_int64
         getattr(lib, f).argtypes = [C.c_int64] * n + ([C.c_int] if f == "need" else [])
+    lib.plan_at.restype, lib.plan_at.argtypes = None, [C.c_int64] * 3 + [C.c_int, C.POINTER(C.c_int64)]
+    lib.at = lambda *a: (lambda o: (lib.plan_at(*a, o), tuple(o))[1])((C.c_int64 * 7)())
     return lib
 
 
@@ -107,3 +115,29 @@ def test_a_byte_too_few_is_refused(plan, M, N, K):
     for f, n in zip(calls, need):
         if n:       # (a call that needs none would be launched)
             assert f(n - 1) == -5 and f" {n} needed" in bqm.bqm_last_error()
+
+
+def drawn(seed, n):
+    rng = random.Random(seed)
+    for _ in range(n):
+        yield int(2 ** rng.uniform(0, 14)), *(max(8, int(2 ** rng.uniform(6, 13)) // 8 * 8) for _ in range(2)), rng.randrange(3)
+
+
+def test_every_step_is_some_part_s(plan):
+    for M, N, K, d in drawn(3, 20000):
+        bm, bn, full, rem, S, per, nk = plan.at(M, N, K, d)
+        I, J, C_ = ((M, N, K), (M, K, N), (N, K, M))[d]
+        assert full + rem == -(-I // bm) * -(-J // bn) and nk == -(-C_ // 64), (M, N, K, d)
+        assert 1 <= S and per * S >= nk > per * (S - 1) and (S == 1 or rem and per >= 2), (M, N, K, d)
+
+
+def test_idle_cus_get_one_part_each(plan):
+    """Where a round's tiles leave CUs idle, their parts are no more than the CUs."""
+    assert plan.at(72, 3064, 472, 1)[4] <= 16
+    split = 0
+    for M, N, K, d in drawn(5, 20000):
+        _, _, full, rem, S, _, _ = plan.at(M, N, K, d)
+        if S > 1 and full + rem <= 256:
+            split += 1
+            assert rem * S <= 256, (M, N, K, d)
+    assert split > 1000
