@@ -576,3 +576,20 @@ def test_past_four_gigabytes_exactly():
         ref += D.T @ X
     assert torch.equal(dw.double(), ref)
     assert torch.equal(db.double(), dz.double().sum(0))
+
+
+# sizes at which workgroups walk more than one tile, or a tile and a part of one: each tile in each
+# direction where the plan does so, with last steps that are whole and that are not (LARGE has some
+# of these only; test_linear_plan.py holds them to the plan)
+ROUNDS = [(7286, 3224, 1344), (1556, 4984, 2416), (5874, 608, 2848), (2325, 2160, 3320), (4078, 1704, 240),
+          (9239, 896, 800), (1318, 1120, 5568), (1173, 3008, 3248), (10956, 2584, 288), (9, 59000, 896), (10, 39776, 864),
+          (10, 33608, 1920), (9, 37664, 2144), (1088, 3104, 2496), (642, 1152, 6752), (7872, 32824, 8), (7218, 33072, 8),
+          (11244, 64, 1320), (9258, 72, 1608), (1264, 2880, 6752), (10980, 2584, 656), (11373, 1304, 64), (10963, 1288, 72),
+          (4615, 3408, 896), (10053, 1544, 800), (64, 3216, 4944), (70, 37928, 264), (3328, 33512, 240), (2071, 64, 7376),
+          (6530, 448, 2456), (331, 33616, 896), (64, 33176, 432), (640, 2232, 7280), (9, 36832, 64), (9, 32856, 72),
+          (11, 33712, 768), (11, 34504, 656), (4544, 37408, 8), (1775, 32984, 8), (10979, 8, 264), (9, 32776, 8), (2049, 2056, 32)]
+
+
+@pytest.mark.parametrize("M,N,K", ROUNDS)
+def test_large_in_rounds(M, N, K):
+    test_large(M, N, K)

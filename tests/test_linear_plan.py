@@ -141,3 +141,30 @@ def test_idle_cus_get_one_part_each(plan):
             split += 1
             assert rem * S <= 256, (M, N, K, d)
     assert split > 1000
+
+
+def test_tested_sizes_reach_every_plan(plan):
+    """Of the sizes that the GPU tests run, some take each tile in each direction: as one round of
+    tiles and as more, whole and with a part split along the contraction, and where the plan does so
+    with both kinds of last step."""
+    from tests.test_gpu_linear import LARGE, ROUNDS, SHAPES
+
+    def kinds(sizes):
+        for M, N, K in sizes:
+            for d in range(3):
+                bm, bn, full, rem, S, _, nk = plan.at(M, N, K, d)
+                C_ = (K, N, M)[d]
+                if d == 0 and M <= 8 and (K <= 4096 or 2 * N >= K):
+                    continue        # not by tiles
+                walks = full > 0 and full + rem * S > (512 if bm == 64 else 256)
+                yield ("fwd", "dgrad", "wgrad")[d], (bm, bn) if C_ >= 64 else "short", walks, S > 1, C_ >= 64 and C_ % 64 > 0
+    got = set(kinds(SHAPES + LARGE + ROUNDS))
+    # what ordinary sizes take
+    usual = {}
+    for M, N, K, _ in drawn(9, 30000):
+        for k in kinds([(M, N, K)]):
+            usual[k] = usual.get(k, 0) + 1
+    missing = {k: n for k, n in usual.items() if n >= 10 and k not in got and k[2]}
+    assert not missing, missing
+    missing = {k[:4] for k in usual if usual[k] >= 10} - {k[:4] for k in got}
+    assert not missing, missing
