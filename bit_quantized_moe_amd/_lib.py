@@ -513,7 +513,8 @@ def bqm_combine(y, inv, out, topk_w=None, residual=None, n_rows=None, stream=Non
 
 
 def bqm_combine_grad(dout, inv, y=None, topk_w=None, dy=None, dtopk_w=None, n_rows=None, stream=None):
-    """dout [T, H] -> dy [R, H] and dtopk_w [T, k] (which needs y [R, H]), where given."""
+    """dout [T, H] -> dy [R, H] and dtopk_w [T, k] (which needs y [R, H]), where given; dy may be
+    y where no two pairs stand at one row."""
     lib, dev = _begin()
     T, H = dout.shape
     R = inv.numel()

@@ -14,9 +14,12 @@
 // What bounds it.  Large products: the power the matrix unit draws (69% busy at a clock of 2.0
 // GHz); 16384 x 4096 x 6144 takes 555 us forward, 570 for the input's and 590 for the weight's
 // gradient, 1.4 to 1.5 PFLOP/s.  The 16x16x32 instruction draws less than the 32x32x16 of the
-// same rate.  Small ones: a CU's copies, about 100 GB/s each (32 KB of a 128 x 128 tile's step
-// in 0.33 us), and 4 to 7 us of launch, first copies and epilogue: 1111 x 2848 x 2080 21 us,
-// 203 x 768 x 2048 8.7 us.  Few rows: the weights' bytes.
+// same rate.  Small ones: 4 to 7 us of launch, first copies and epilogue, and steps in which the
+// copies take about as long as the fragment reads and products beside them: 1111 x 2848 x 2080, one
+// round of 128 x 128 tiles, takes 21.0 us, without its copies 19.0, without its products 20.1, without
+// both (fragment reads, waits, barriers) 13.0; where rows start on 128 bytes (2048 in place of 2080) the
+// copies are hidden, 17.9 us in all.  64 x 64 tiles: a CU's copies, 85 GB/s (16 KB of a step in 0.19
+// us); 203 x 768 x 2048 8.7 us.  Few rows: the weights' bytes.
 #include "common.h"
 #include "linear_plan.h"
 
@@ -949,14 +952,15 @@ __global__ void __launch_bounds__(256) join_parts(LinParams p) {
 // row takes 30.8 us, 27.7 through them); lanes without a row of x load none (with all of them 4096 x
 // 6144 takes 12.2 us instead of 11.6: 4.3 TB/s).
 //
-// 1, 4 and 8 rows, against the 64-row tile, in us, weights from HBM: of 4096 x 6144 11.6, 12.6 and
-// 13.9 against 15.1; of 8192 x 8192 27.6, 27.8 and 29.5 against 33.4; of 6144 x 2048 8.0, 8.5 and
-// 9.3 against 8.7; of 768 x 2048 4.8, 5.1 and 5.5 against 7.4; of 256 x 1024 3.4, 3.5 and 3.7
-// against 5.3; with 16 rows of these 15.9, 35.3, 10.3, 6.3 and 4.0.  A workgroup's stream takes 1.0
-// us per 1024 of the contraction, so that where few of them have long rows the tiles, which split
-// the contraction over idle CUs, are ahead: 1, 4 and 8 rows of 1024 x 8192 11.3, 12.7 and 14.2
-// against 9.6, of 2048 x 8192 12.1, 13.4 and 14.9 against 11.7; of 1024 x 4096 7.1, 7.8 and 8.5
-// against 8.5.
+// 1, 4 and 8 rows, against tiles, in us, weights from HBM (copies of 600 MB in all, in turn): of 4096
+// x 6144 12.0, 13.4 and 14.6 against 15.9; of 8192 x 8192 32.5, 30.7 and 32.4 against 37.5; of 6144 x
+// 2048 9.1, 9.2 and 9.9 against 12.2; of 768 x 2048 5.3, 5.6 and 6.0 against 8.8; of 256 x 1024 3.8,
+// 4.0 and 4.1 against 5.6; of 1024 x 4096 7.7, 8.4 and 9.0 against 9.5; with 16 rows of these 17.5,
+// 38.3, 11.0, 6.7, 4.5 and 10.2.  From the last-level cache one row of 4096 x 6144 takes 9.9, and 8 of
+// 6144 x 2048 9.3 where tiles take 8.7.  A workgroup's stream takes 1.0 us per 1024 of the contraction,
+// so that where few of them have long rows the tiles, which split the contraction over idle CUs, are
+// ahead: 1, 4 and 8 rows of 1024 x 8192 12.1, 13.3 and 14.7 against 10.8, of 2048 x 8192 14.0, 14.4
+// and 15.5 against 12.8.
 constexpr int FW = 8, FU = 4;  // waves; MFMA steps of 32 per group
 
 __global__ void __launch_bounds__(64 * FW) lin_few(LinParams p) {

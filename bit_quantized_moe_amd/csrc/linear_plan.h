@@ -18,8 +18,10 @@ inline bool few_rows(int64_t M, int64_t N, int64_t K) { return M <= kFewRows && 
 
 // The tile and its split by what they are expected to take: per round of tiles, the steps of 64
 // and the rest (launch, first copies, epilogue), both measured with every CU busy, and for a split
-// the parts written and read and the join's launch.  Both sides, in us (tiles of 256 x 256, 256 x
-// 128, 128 x 128, 64 x 64, each in the split that is best for it):
+// the parts written and read and the join's launch.  It ranks tiles rather than foretells times: the
+// rest is charged to every round, launch and all, and with idle CUs a step is shorter (37 x 6144 x
+// 2048 is expected at 11.8 us and takes 8.9).  Both sides, in us (tiles of 256 x 256, 256 x 128, 128 x
+// 128, 64 x 64, each in the split that is best for it):
 //   forward 37 x 6144 x 2048          15.0  13.0  12.3   8.9
 //           300 x 2048 x 2048         26.4  20.0  15.9   9.0
 //           1111 x 2848 x 2080        36.6  28.9  21.0  34.2

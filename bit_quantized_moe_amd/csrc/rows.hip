@@ -11,9 +11,11 @@
 // gradient), and HBM bounds them.  A lane holds 8 consecutive elements (16-byte accesses;
 // one element where H is no multiple of 8) of the token and of several of its rows at a
 // time, all loaded before the first is used.  The experts' rows are read, and all results
-// written, past the caches, the tokens' rows are read through them: 16384 x 8 x 6144, dispatch
-// 307 us (379 with everything past them, 366 with nothing), combine 309 (355, 392), gradient
-// 640 (680, 687), which are 5.9, 6.5 and 5.3 TB/s.
+// written, past the caches, the tokens' rows are read through them: 16384 x 8 x 6144 without
+// dropped pairs, dispatch 307 us (379 with everything past them, 366 with nothing), combine with a
+// residual 309 (355, 392), gradient 640 (680, 687), which are 5.9, 6.5 and 5.3 TB/s.  With 5% of the
+// pairs dropped 298, 296 and 597 us, 5.8, 6.5 and 5.5 TB/s of what is then moved.  One element per
+// lane: 16384 x 8 x 6145 868, 879 and 961 us, 2.1, 2.3 and 3.6 TB/s.
 #include "common.h"
 
 namespace bqm {

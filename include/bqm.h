@@ -320,7 +320,8 @@ bqm_status bqm_combine(const uint16_t *y, const int32_t *inv, const float *topk_
                        int64_t H, int32_t k, const int32_t *n_rows, uint16_t *out, void *stream);
 
 /* Its gradient, dout bf16 [T, H] (which is also the residual's):
- *   dy[inv[f]] = topk_w[f] dout[t]      -> bf16 [R, H], or NULL; may be y
+ *   dy[inv[f]] = topk_w[f] dout[t]      -> bf16 [R, H], or NULL; may be y where no two pairs
+ *                                          stand at one row (the second would read the first's dy)
  *   dtopk_w[f] = <dout[t], y[inv[f]]>   -> f32 [T, k], or NULL (y is then not read); 0 for
  *                                          dropped pairs */
 bqm_status bqm_combine_grad(const uint16_t *dout, const uint16_t *y, const int32_t *inv, const float *topk_w, int64_t T,
