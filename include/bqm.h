@@ -304,9 +304,10 @@ bqm_status bqm_router_grad(const float *logits, const int32_t *topk_idx, const u
  * the expert-ordered tensors [R, H], R = T * k.  Pairs with inv[f] < 0 or inv[f] >= n are
  * dropped: n = *n_rows (device int32, for instance offsets + E; 4-byte aligned), at most R,
  * or R where n_rows is NULL.  Nothing is read or written for a dropped pair, and the rows that
- * no pair stands at are left as they were.  Two pairs at one row get one's result or the
- * other's.  1 <= H < 2^24 (16-byte accesses where 8 divides H), k >= 1, T * k < 2^31; T == 0
- * is a no-op.  topk_w f32 [T, k], NULL: 1.  Sums are FP32 in the order of j. */
+ * no pair stands at are left as they were.  Where two pairs stand at one row, each of its
+ * elements is one's result or the other's.  1 <= H < 2^24 (16-byte accesses where 8 divides H),
+ * k >= 1, T * k < 2^31; T == 0 is a no-op.  topk_w f32 [T, k], NULL: 1.  Sums are FP32 in the
+ * order of j. */
 
 /* rows[inv[f]] = x[t]: a token's row at the place of each of its pairs, as the experts'
  * products without perm, or an exchange between devices, read them.  Its gradient is
